@@ -39,7 +39,7 @@
  * Conventions for every entry point:
  *   - All pointers are device pointers unless marked "host".  The caller owns
  *     every buffer; the library never allocates, frees or synchronises in the
- *     hot calls (ngram_hash, ngram_embed_fwd, ngram_embed_bwd_accum,
+ *     hot calls (ngram_hash, ngram_embed_fwd, ngram_embed_fwd_drop, ngram_embed_bwd_accum,
  *     ngram_embed_bwd_step, ngram_window_keys, ngram_window_sort,
  *     ngram_window_reduce, ngram_sparse_step, ngram_window_export,
  *     ngram_touched_rows and the _dev step variants).  Those calls only enqueue work on `stream` (a
@@ -64,6 +64,8 @@
 #define NGRAM_H
 
 #include <stdint.h>
+
+#include "drop.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -228,6 +230,19 @@ int ngram_hash(const ngram_config *cfg, const int32_t *tokens, int64_t T,
 int ngram_embed_fwd(const ngram_config *cfg, const void *W_b, const void *W_t,
                     const int32_t *tokens, int64_t T, void *out, void *ws,
                     void *stream);
+
+/* ngram_embed_fwd with its output dropped in the same pass (drop.h):
+ *   out[i][j] = k[i][j] c (s_b W_b[r_b(i)][j] + s_t W_t[r_t(i)][j]),
+ * k and c those of a [T][768] tensor under `spec` (host); the sum and the
+ * scaling in fp32, one rounding to out's dtype (bf16: nearest, ties to even;
+ * a NaN stays a NaN).  Arguments, options and flags as for ngram_embed_fwd.
+ * Its backward is drop_bwd of dY under the same spec and shape (in place, if
+ * the caller likes), then the calls below with the result.  A bad spec gives
+ * NGRAM_ENULL, NGRAM_EARG or NGRAM_EALIGN. */
+int ngram_embed_fwd_drop(const ngram_config *cfg, const void *W_b,
+                         const void *W_t, const int32_t *tokens, int64_t T,
+                         const drop_spec *spec, void *out, void *ws,
+                         void *stream);
 
 /* Backward of one micro-step into the window accumulator (gradients are
  * accumulated over accum_steps micro-steps and applied once: the

@@ -1,0 +1,31 @@
+"""Checks of tensors and the stream of a call, shared by the bindings of
+``drop``, ``ffn`` and ``ngram.embed_fwd_drop``.
+
+A call runs on its tensors' device, on that device's current stream, whatever
+device is current in the calling thread."""
+from __future__ import annotations
+
+import torch
+
+
+def ptr(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None) -> int:
+    """The address of a contiguous GPU tensor on `device`, after the checks."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def enqueue(f, device: torch.device, *args) -> int:
+    """f(*args, stream) on the device's current stream; its status."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        return f(*args, torch.cuda.current_stream(device).cuda_stream)

@@ -12,6 +12,7 @@
 
 #include "../../include/ngram.h"
 #include "ngram_dev.hpp"
+#include "philox.hpp"
 
 using namespace ngram;
 
@@ -298,6 +299,27 @@ int ngram_embed_fwd(const ngram_config *cfg, const void *W_b, const void *W_t, c
     return hip_status(launch_fwd(cfg->dtype, (cfg->options & NGRAM_OPT_OUT_F32) != 0, hash_params(cfg), W_b, W_t,
                                  tokens, T, out, flags_of(ws),
                                  (hipStream_t)stream));
+}
+
+int ngram_embed_fwd_drop(const ngram_config *cfg, const void *W_b, const void *W_t, const int32_t *tokens,
+                         int64_t T, const drop_spec *spec, void *out, void *ws, void *stream)
+{
+    int rc = check_cfg(cfg);
+    if (rc)
+        return rc;
+    if ((rc = check_tokens(cfg, tokens, T)))
+        return rc;
+    static_assert(DROP_ENULL == NGRAM_ENULL && DROP_EALIGN == NGRAM_EALIGN && DROP_EARG == NGRAM_EARG,
+                  "a spec's errors are this header's");
+    if ((rc = drop::check_spec(spec)))
+        return rc;
+    const bool direct = (cfg->options & NGRAM_OPT_DIRECT) != 0;   // W_t is not used then
+    if (!W_b || (!W_t && !direct) || (T > 0 && !out))
+        return NGRAM_ENULL;
+    if (!aligned(W_b, 16) || !aligned(W_t, 16) || !aligned(out, 16) || !aligned(ws, kAlign))
+        return NGRAM_EALIGN;
+    return hip_status(launch_fwd_drop(cfg->dtype, (cfg->options & NGRAM_OPT_OUT_F32) != 0, hash_params(cfg), W_b,
+                                      W_t, tokens, T, *spec, out, flags_of(ws), (hipStream_t)stream));
 }
 
 int ngram_embed_bwd_accum(const ngram_config *cfg, void *ws, const int32_t *tokens, const void *dY,

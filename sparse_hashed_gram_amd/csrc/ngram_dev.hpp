@@ -10,6 +10,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/drop.h"
+
 namespace ngram {
 
 constexpr int kDim = 768;
@@ -493,6 +495,9 @@ hipError_t launch_hash(const HashParams &hp, const int32_t *tok, int64_t T, uint
                        uint32_t *flags, hipStream_t s);
 hipError_t launch_fwd(int dtype, bool out_f32, const HashParams &hp, const void *wb, const void *wt,
                       const int32_t *tok, int64_t T, void *out, uint32_t *flags, hipStream_t s);
+hipError_t launch_fwd_drop(int dtype, bool out_f32, const HashParams &hp, const void *wb, const void *wt,
+                           const int32_t *tok, int64_t T, const drop_spec &spec, void *out, uint32_t *flags,
+                           hipStream_t s);
 
 // Burst: keep one micro-step (packed indices + dY rows) in the stash.
 hipError_t launch_stash(const WsLayout &L, uint8_t *ws, const HashParams &hp,

@@ -12,6 +12,9 @@ import os
 
 import torch
 
+from . import _marshal
+from .drop import DropSpec, _check_rng
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libngram.so")
 
 DTYPE_F32 = 0
@@ -129,6 +132,7 @@ def lib() -> ctypes.CDLL:
             "ngram_workspace_init": ([cp, vp, ctypes.c_uint64, vp], ctypes.c_int),
             "ngram_hash": ([cp, vp, i64, vp, vp, vp], ctypes.c_int),
             "ngram_embed_fwd": ([cp, vp, vp, vp, i64, vp, vp, vp], ctypes.c_int),
+            "ngram_embed_fwd_drop": ([cp, vp, vp, vp, i64, ctypes.POINTER(DropSpec), vp, vp, vp], ctypes.c_int),
             "ngram_embed_bwd_accum": ([cp, vp, vp, vp, i64, vp], ctypes.c_int),
             "ngram_window_reduce": ([cp, vp, vp], ctypes.c_int),
             "ngram_window_keys": ([cp, vp, vp, i64, vp], ctypes.c_int),
@@ -268,6 +272,27 @@ def embed_fwd(cfg: NgramConfig, W_b: torch.Tensor, W_t: torch.Tensor, tokens: to
     _check("ngram_embed_fwd", lib().ngram_embed_fwd(
         ctypes.byref(cfg), _dev(W_b, "W_b", cfg.torch_dtype), _dev(W_t, "W_t", cfg.torch_dtype),
         _dev(tokens, "tokens", torch.int32), T, _dev(out, "out", cfg.out_torch_dtype), _ws(ws), _stream()))
+    return out
+
+
+def embed_fwd_drop(cfg: NgramConfig, W_b: torch.Tensor, W_t: torch.Tensor | None, tokens: torch.Tensor,
+                   spec: DropSpec, out: torch.Tensor | None = None, ws: Workspace | None = None) -> torch.Tensor:
+    """embed_fwd with its output dropped in the same pass (drop.spec).  Its
+    backward: drop.bwd(spec, dY, out=dY), then embed_bwd_accum or
+    embed_bwd_step with the result."""
+    T = tokens.numel()
+    dev = tokens.device
+    _check_tables(cfg, W_b, W_t)
+    if out is None:
+        out = torch.empty((T, DIM), dtype=cfg.out_torch_dtype, device=dev)
+    pw = None if W_t is None else _marshal.ptr(W_t, "W_t", dev, cfg.torch_dtype)
+    po = _marshal.ptr(out, "out", dev, cfg.out_torch_dtype, (T, DIM))
+    if ws is not None and ws.tensor.device != dev:
+        raise ValueError(f"the workspace is on {ws.tensor.device}, the tokens on {dev}")
+    _check_rng(spec, dev)
+    _check("ngram_embed_fwd_drop", _marshal.enqueue(
+        lib().ngram_embed_fwd_drop, dev, cfg, _marshal.ptr(W_b, "W_b", dev, cfg.torch_dtype), pw,
+        _marshal.ptr(tokens, "tokens", dev, torch.int32), T, spec, po, _ws(ws)))
     return out
 
 
