@@ -1,6 +1,6 @@
 """Builds libngram.so (HIP, gfx950) in-tree with hipcc: the n-gram table
-(include/ngram.h), the sampled-softmax loss (include/ssm.h) and counter-based
-dropout (include/drop.h).
+(include/ngram.h), the sampled-softmax loss (include/ssm.h), counter-based
+dropout (include/drop.h) and the gated feed-forward block (include/ffn.h).
 
     python -m sparse_hashed_gram_amd.build
 
@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libngram.so")
 SOURCES = ["ngram_abi.hip", "ngram_fwd.hip", "ngram_reduce.hip", "ngram_step.hip", "ngram_drop.hip", "ssm.hip",
-           "drop.hip"]
+           "drop.hip", "ffn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
