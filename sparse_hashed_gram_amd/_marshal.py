@@ -7,6 +7,10 @@ from __future__ import annotations
 
 import torch
 
+# the stream's handle without the object around it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def ptr(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None) -> int:
     """The address of a contiguous GPU tensor on `device`, after the checks."""
@@ -26,6 +30,6 @@ def ptr(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None
 def enqueue(f, device: torch.device, *args) -> int:
     """f(*args, stream) on the device's current stream; its status."""
     if device.index == torch.cuda.current_device():
-        return f(*args, torch.cuda.current_stream(device).cuda_stream)
+        return f(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
-        return f(*args, torch.cuda.current_stream(device).cuda_stream)
+        return f(*args, _raw_stream(device.index))

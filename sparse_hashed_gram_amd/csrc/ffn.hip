@@ -165,9 +165,31 @@ __device__ __forceinline__ float act(float g, float &d)
 
 // ------------------------------------------------------------------ kernels
 
-// Tiles: WM x WN matrix-core tiles of 32 x 32 per wavefront, 2 x 2 wavefronts.
-constexpr int kWM = 2, kWN = 2, kGM = 2, kGN = 2, kNS = 2, kThreads = 64 * kGM * kGN;
-constexpr int kBM = 32 * kWM * kGM, kBN = 32 * kWN * kGN;
+// Block tiles of BM x BN: GM x GN wavefronts of WM x WN matrix-core tiles of 32 x 32.
+template <int WM_, int WN_, int GM_, int GN_>
+struct Shape {
+    static constexpr int WM = WM_, WN = WN_, GM = GM_, GN = GN_, NW = GM * GN, THREADS = 64 * NW;
+    static constexpr int BM = 32 * WM * GM, BN = 32 * WN * GN;
+    static constexpr bool BIG = NW == 8;
+
+    template <bool AK, bool BK, int M>
+    static constexpr uint32_t smem()
+    {
+        return Tile<AK, BK, M, WN, GM, GN>::SMEM;
+    }
+
+    template <bool AK, bool BK, int M>
+    static __device__ __forceinline__ void run(const Operand &A, const Operand &B, int64_t k0, int64_t K,
+                                               uint8_t *sm, f32x16 (&acc)[M][WN])
+    {
+        product<AK, BK, M, WN, GM, GN>(A, B, (int32_t)k0, (int32_t)K, sm, acc);
+    }
+};
+using Half = Shape<2, 1, 2, 2>;     // 128 x 64, 4 wavefronts, three blocks per CU
+using Small = Shape<2, 2, 2, 2>;    // 128 x 128, 4 wavefronts, two blocks per CU
+using Mid = Shape<2, 3, 2, 2>;      // 128 x 192, 4 wavefronts, two blocks per CU (81,920 bytes of LDS each)
+using Wide = Shape<2, 3, 4, 2>;     // 256 x 192, 8 wavefronts
+using Square = Shape<4, 2, 2, 4>;   // 256 x 256, 8 wavefronts
 
 struct Args {
     const uint16_t *X, *Wg, *Wu, *Wd, *dY;
@@ -177,45 +199,46 @@ struct Args {
     const void *res;
     void *out;
     int32_t out_f32;
+    int32_t parts;           // parts of k of a [T][768] result
+    float *part;             // [parts][T][768] where parts > 1
     drop::Mask mask;
 };
 
 __device__ __forceinline__ Operand rows_of(const uint16_t *p, int64_t ld, int64_t first, int64_t count, int64_t k)
 {
-    return Operand{{p, p}, ld, first, count, INT64_MAX, k, 0};
+    return Operand{{p, p}, ld, first, count, INT32_MAX, (int32_t)k, 0};
 }
 
 constexpr uint32_t cmax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-template <int MB>
+template <class S, int MB>
 constexpr uint32_t smem_for(uint32_t main)
 {
-    return cmax(main, kGM * kGN * Rows<MB>::BYTES);
+    return cmax(main, S::NW * Rows<MB>::BYTES);
 }
 
-// H tile of kBN positions x kBM / 2 hidden units: each wavefront holds its
+// H tile of BN positions x BM / 2 hidden units: each wavefront holds its
 // units' gate sums in the first half of its m-blocks and the up sums in the
 // second, so both meet in one lane.
-template <int ACT>
-__global__ __launch_bounds__(kThreads) void up_kernel(Args a)
+template <class S, int ACT>
+__global__ __launch_bounds__(S::THREADS) void up_kernel(Args a)
 {
-    using T0 = Tile<false, false, kWM, kWN, kGM, kGN, kNS>;
-    constexpr int HB = kWM / 2;
-    __shared__ __align__(16) uint8_t sm[smem_for<HB>(T0::SMEM)];
+    constexpr int HB = S::WM / 2;
+    __shared__ __align__(16) uint8_t sm[smem_for<S, HB>(S::template smem<false, false, S::WM>())];
     uint32_t tt, ot;
     if (!tile_of(a.tiles_t, a.tiles_o, tt, ot))
         return;
-    const int64_t n0 = (int64_t)tt * kBN, f0 = (int64_t)ot * (kBM / 2);
-    f32x16 acc[kWM][kWN];
+    const int64_t n0 = (int64_t)tt * S::BN, f0 = (int64_t)ot * (S::BM / 2);
+    f32x16 acc[S::WM][S::WN];
     clear(acc);
-    const Operand A{{a.Wg, a.Wu}, kD, f0, a.F, INT64_MAX, kD, 32 * HB};
-    product<false, false, kWM, kWN, kGM, kGN, kNS>(A, rows_of(a.X, kD, n0, a.T, kD), kD, sm, acc);
-    const int w = threadIdx.x >> 6, wm = w / kGN, wn = w % kGN;
+    const Operand A{{a.Wg, a.Wu}, kD, f0, a.F, INT32_MAX, kD, 32 * HB};
+    S::template run<false, false, S::WM>(A, rows_of(a.X, kD, n0, a.T, kD), 0, kD, sm, acc);
+    const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
     float *lds = reinterpret_cast<float *>(sm + w * Rows<HB>::BYTES);
     const int64_t fw = f0 + wm * 32 * HB;
 #pragma unroll
-    for (int nb = 0; nb < kWN; ++nb) {
-        const int64_t tw = n0 + (wn * kWN + nb) * 32;
+    for (int nb = 0; nb < S::WN; ++nb) {
+        const int64_t tw = n0 + (wn * S::WN + nb) * 32;
         Rows<HB>::write(
             lds,
             [&](int mb, int e) {
@@ -230,82 +253,126 @@ __global__ __launch_bounds__(kThreads) void up_kernel(Args a)
     }
 }
 
-// A [T][768] result: DX false: Y = (res +) drop(H Wd^T); true: dX = [dG | dU] [Wg; Wu].
+// dropout, residual, rounding: 8 results of element i on of Y or dX
 template <bool DX>
-__global__ __launch_bounds__(kThreads) void rows_kernel(Args a)
+__device__ __forceinline__ void put_rows(const Args &a, const drop::Key &key, int64_t i, float (&v)[8])
 {
-    using T0 = Tile<DX, false, kWM, kWN, kGM, kGN, kNS>;
-    __shared__ __align__(16) uint8_t sm[smem_for<kWM>(T0::SMEM)];
+    if (!DX && a.mask.thr != 0) {
+        const uint4 bits = drop::bits_of(key, (uint64_t)i / 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = drop::dropped(v[e], bits, e, a.mask.thr, a.mask.scale);
+    }
+    if (!DX && a.res) {
+        float r[8];
+        load_as(a.res, a.out_f32, i, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += r[e];
+    }
+    store_as(a.out, a.out_f32, i, v);
+}
+
+// A [T][768] result: DX false: Y = (res +) drop(H Wd^T); true: dX = [dG | dU] [Wg; Wu].
+// With parts of k, each block's sums go to the workspace and rows_reduce_kernel ends the pass.
+template <class S, bool DX>
+__global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
+{
+    __shared__ __align__(16) uint8_t sm[smem_for<S, S::WM>(S::template smem<DX, false, S::WM>())];
     uint32_t tt, ot;
-    if (!tile_of(a.tiles_t, a.tiles_o, tt, ot))
+    if (!tile_of(a.tiles_t, a.tiles_o * (uint32_t)a.parts, tt, ot))
         return;
-    const int64_t n0 = (int64_t)tt * kBN, d0 = (int64_t)ot * kBM;
-    f32x16 acc[kWM][kWN];
+    const uint32_t part = ot / a.tiles_o;
+    ot -= part * a.tiles_o;
+    const int64_t n0 = (int64_t)tt * S::BN, d0 = (int64_t)ot * S::BM;
+    const int64_t nk = (DX ? 2 * a.Fp : a.Fp) / kBK, k0 = part * nk / a.parts * kBK, k1 = (part + 1) * nk / a.parts * kBK;
+    f32x16 acc[S::WM][S::WN];
     clear(acc);
     if constexpr (DX) {
-        const Operand A{{a.Wg, a.Wu}, kD, d0, kD, a.Fp, a.F, 0};
-        const Operand B{{a.S, a.S}, 3 * a.Fp, n0, a.T, a.Fp, a.F, 0};
-        product<true, false, kWM, kWN, kGM, kGN, kNS>(A, B, 2 * a.Fp, sm, acc);
+        const Operand A{{a.Wg, a.Wu}, kD, d0, kD, (int32_t)a.Fp, (int32_t)a.F, 0};
+        const Operand B{{a.S, a.S}, 3 * a.Fp, n0, a.T, (int32_t)a.Fp, (int32_t)a.F, 0};
+        S::template run<true, false, S::WM>(A, B, k0, k1 - k0, sm, acc);
     } else {
-        product<false, false, kWM, kWN, kGM, kGN, kNS>(rows_of(a.Wd, a.F, d0, kD, a.F),
-                                                       rows_of(a.S, a.Fp, n0, a.T, a.F), a.Fp, sm, acc);
+        S::template run<false, false, S::WM>(rows_of(a.Wd, a.F, d0, kD, a.F), rows_of(a.S, a.Fp, n0, a.T, a.F), k0,
+                                             k1 - k0, sm, acc);
     }
-    const int w = threadIdx.x >> 6, wm = w / kGN, wn = w % kGN;
-    float *lds = reinterpret_cast<float *>(sm + w * Rows<kWM>::BYTES);
+    const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
+    float *lds = reinterpret_cast<float *>(sm + w * Rows<S::WM>::BYTES);
     const drop::Key key = drop::key_of(a.mask);
+    float *pp = a.parts > 1 ? a.part + part * (a.T * kD) : nullptr;
 #pragma unroll
-    for (int nb = 0; nb < kWN; ++nb) {
-        const int64_t tw = n0 + (wn * kWN + nb) * 32, dw = d0 + wm * 32 * kWM;
-        Rows<kWM>::write(
+    for (int nb = 0; nb < S::WN; ++nb) {
+        const int64_t tw = n0 + (wn * S::WN + nb) * 32, dw = d0 + wm * 32 * S::WM;
+        Rows<S::WM>::write(
             lds, [&](int mb, int e) { return acc[mb][nb][e]; },
             [&](int n, int m, float (&v)[8]) {
                 const int64_t t = tw + n, i = t * kD + dw + m;
                 if (t >= a.T)
                     return;
-                if (!DX && a.mask.thr != 0) {
-                    const uint4 bits = drop::bits_of(key, (uint64_t)i / 8);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = drop::dropped(v[e], bits, e, a.mask.thr, a.mask.scale);
-                }
-                if (!DX && a.res) {
-                    float r[8];
-                    load_as(a.res, a.out_f32, i, r);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] += r[e];
-                }
-                store_as(a.out, a.out_f32, i, v);
+                if (pp)
+                    store_as(pp, true, i, v);
+                else
+                    put_rows<DX>(a, key, i, v);
             });
     }
 }
 
-// dG, dU and H of kBN positions x kBM / 2 hidden units: the gate and up sums
-// again as in up_kernel, then dH of the same tile.
-template <int ACT>
-__global__ __launch_bounds__(kThreads) void grad_kernel(Args a)
+// v += the parts' 8 values at i, in order; four parts' loads at a time are in flight.
+__device__ __forceinline__ void add_parts(const float *part, int64_t size, int parts, int64_t i, float (&v)[8])
 {
-    constexpr int HB = kWM / 2;
-    using T0 = Tile<false, false, kWM, kWN, kGM, kGN, kNS>;
-    using T1 = Tile<true, false, HB, kWN, kGM, kGN, kNS>;
-    __shared__ __align__(16) uint8_t sm[smem_for<HB>(cmax(T0::SMEM, T1::SMEM))];
+    for (int p = 0; p < parts; p += 4) {
+        float x[4][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (p + q < parts)
+                load_as(part + (p + q) * size, true, i, x[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (p + q < parts) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] += x[q][e];
+            }
+    }
+}
+
+// The parts of k, added in order, then the same end as rows_kernel's.
+template <bool DX>
+__global__ __launch_bounds__(256) void rows_reduce_kernel(Args a)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= a.T * kD)
+        return;
+    float v[8] = {};
+    add_parts(a.part, a.T * kD, a.parts, i, v);
+    put_rows<DX>(a, drop::key_of(a.mask), i, v);
+}
+
+// dG, dU and H of BN positions x BM / 2 hidden units: the gate and up sums
+// again as in up_kernel, then dH of the same tile.
+template <class S, int ACT>
+__global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
+{
+    constexpr int HB = S::WM / 2;
+    __shared__ __align__(16) uint8_t sm[smem_for<S, HB>(
+        cmax(S::template smem<false, false, S::WM>(), S::template smem<true, false, HB>()))];
     uint32_t tt, ot;
     if (!tile_of(a.tiles_t, a.tiles_o, tt, ot))
         return;
-    const int64_t n0 = (int64_t)tt * kBN, f0 = (int64_t)ot * (kBM / 2);
-    f32x16 acc[kWM][kWN], dh[HB][kWN];
+    const int64_t n0 = (int64_t)tt * S::BN, f0 = (int64_t)ot * (S::BM / 2);
+    f32x16 acc[S::WM][S::WN], dh[HB][S::WN];
     clear(acc);
+    const Operand A{{a.Wg, a.Wu}, kD, f0, a.F, INT32_MAX, kD, 32 * HB};
+    S::template run<false, false, S::WM>(A, rows_of(a.X, kD, n0, a.T, kD), 0, kD, sm, acc);
     clear(dh);
-    const Operand A{{a.Wg, a.Wu}, kD, f0, a.F, INT64_MAX, kD, 32 * HB};
-    product<false, false, kWM, kWN, kGM, kGN, kNS>(A, rows_of(a.X, kD, n0, a.T, kD), kD, sm, acc);
-    product<true, false, HB, kWN, kGM, kGN, kNS>(rows_of(a.Wd, a.F, f0, a.F, kD),
-                                                 rows_of(a.dY, kD, n0, a.T, kD), kD, sm, dh);
-    const int w = threadIdx.x >> 6, wm = w / kGN, wn = w % kGN;
+    S::template run<true, false, HB>(rows_of(a.Wd, a.F, f0, a.F, kD),
+                                                 rows_of(a.dY, kD, n0, a.T, kD), 0, kD, sm, dh);
+    const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
     float *lds = reinterpret_cast<float *>(sm + w * Rows<HB>::BYTES);
     const int64_t fw = f0 + wm * 32 * HB;
 #pragma unroll
-    for (int nb = 0; nb < kWN; ++nb) {
-        const int64_t tw = n0 + (wn * kWN + nb) * 32;
+    for (int nb = 0; nb < S::WN; ++nb) {
+        const int64_t tw = n0 + (wn * S::WN + nb) * 32;
         auto put = [&](int which) {
             return [&, which](int n, int m, const float (&v)[8]) {
                 const int64_t t = tw + n, f = fw + m;
@@ -328,6 +395,134 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(Args a)
         Rows<HB>::write(lds, [&](int mb, int e) { return acc[mb][nb][e]; }, put(1));
         Rows<HB>::write(lds, [&](int mb, int e) { return acc[mb + HB][nb][e]; }, put(0));
     }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Up to 64 positions: the weights' bytes bound the pass, and the latency of
+// one round of loads most of it.  No LDS stages and no k loop over barriers:
+// every wavefront loads its share of k straight into matrix-core fragments
+// (16 weight rows x 16 positions x 32 values of k each), all loads in flight at
+// once, and the wavefronts' sums meet in LDS.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+constexpr int kFewWaves = 4, kFewRows = 64;
+constexpr int kFewDown = 8;   // wavefronts of a down block
+
+// H of 16 hidden units, NT tiles of 16 positions; a wavefront takes a quarter of k.
+template <int ACT, int NT>
+__global__ __launch_bounds__(64 * kFewWaves) void up_few_kernel(Args a)
+{
+    constexpr int STEPS = kD / (32 * kFewWaves);   // 6
+    __shared__ __align__(16) f32x4 red[kFewWaves][2][NT][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15;
+    const int64_t f0 = (int64_t)blockIdx.x * 16, f = f0 + r < a.F ? f0 + r : a.F - 1;
+    const int k = w * (kD / kFewWaves) + 8 * (lane >> 4);
+    const uint16_t *pg = a.Wg + f * kD + k, *pu = a.Wu + f * kD + k;
+    bf16x8 g[STEPS], u[STEPS];
+    f32x4 ag[NT] = {}, au[NT] = {};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        g[s] = *reinterpret_cast<const bf16x8 *>(pg + 32 * s);
+        u[s] = *reinterpret_cast<const bf16x8 *>(pu + 32 * s);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int64_t t = 16 * n + r < a.T ? 16 * n + r : a.T - 1;
+        const uint16_t *px = a.X + t * kD + k;
+        bf16x8 x[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            x[s] = *reinterpret_cast<const bf16x8 *>(px + 32 * s);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            ag[n] = mfma16(g[s], x[s], ag[n]);
+            au[n] = mfma16(u[s], x[s], au[n]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        red[w][0][n][lane] = ag[n];
+        red[w][1][n][lane] = au[n];
+    }
+    __syncthreads();
+    if (w >= NT)
+        return;
+    f32x4 sg = red[0][0][w][lane], su = red[0][1][w][lane];
+#pragma unroll
+    for (int p = 1; p < kFewWaves; ++p) {
+        sg += red[p][0][w][lane];
+        su += red[p][1][w][lane];
+    }
+    // lane: position 16 w + lane % 16, units 4 (lane / 16) .. + 3
+    const int64_t t = 16 * w + r, ff = f0 + 4 * (lane >> 4);
+    if (t < a.T && ff < a.F) {
+        float h[4], d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = act<ACT, false>(sg[e], d) * su[e];
+        uint2 o;
+        o.x = ngram::bf16_pack_rne(h[0], h[1]);
+        o.y = ngram::bf16_pack_rne(h[2], h[3]);
+        *reinterpret_cast<uint2 *>(a.S + t * a.Fp + ff) = o;
+    }
+}
+
+// Y of 16 outputs; a wavefront takes every eighth step of 32 values of k.
+template <int NT>
+__global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
+{
+    constexpr int U = 4;   // steps in flight
+    __shared__ __align__(16) f32x4 red[kFewDown][NT][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15;
+    const int64_t d0 = (int64_t)blockIdx.x * 16;
+    const uint16_t *pw = a.Wd + (d0 + r) * a.F;
+    const uint16_t *ph[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        ph[n] = a.S + (16 * n + r < a.T ? 16 * n + r : a.T - 1) * a.Fp;
+    f32x4 acc[NT] = {};
+    const bf16x8 zero = {};
+    for (int64_t k0 = (int64_t)w * 32 + 8 * (lane >> 4); k0 - 8 * (lane >> 4) < a.F; k0 += U * kFewDown * 32) {
+        bf16x8 x[U], h[U][NT];
+#pragma unroll
+        for (int s = 0; s < U; ++s) {
+            const int64_t k = k0 + s * (kFewDown * 32);
+            const bool in = k < a.F;
+            x[s] = in ? *reinterpret_cast<const bf16x8 *>(pw + k) : zero;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                h[s][n] = in ? *reinterpret_cast<const bf16x8 *>(ph[n] + k) : zero;
+        }
+#pragma unroll
+        for (int s = 0; s < U; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[n] = mfma16(x[s], h[s][n], acc[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        red[w][n][lane] = acc[n];
+    __syncthreads();
+    // one thread: 8 outputs of one position, the halves of two lanes of the sums
+    const int n = threadIdx.x / 32, q = threadIdx.x % 32;
+    const int64_t t = 16 * n + q % 16;
+    if (n >= NT || t >= a.T)
+        return;
+    const int from = q % 16 + 32 * (q / 16);   // lanes from and from + 16
+    f32x4 lo = red[0][n][from], hi = red[0][n][from + 16];
+#pragma unroll
+    for (int p = 1; p < kFewDown; ++p) {
+        lo += red[p][n][from];
+        hi += red[p][n][from + 16];
+    }
+    float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    put_rows<false>(a, drop::key_of(a.mask), t * kD + d0 + 8 * (q / 16), v);
 }
 
 struct DwArgs {
@@ -360,10 +555,10 @@ __device__ __forceinline__ void put_dw(const DwArgs &a, void *dst, int64_t i, fl
 // One tile of one part of k: rows n of the result with m contiguous.
 //   dWg | dWu: n = f of 2 Fp (B = dG | dU), m = d (A = X)
 //   dWd:       n = d (B = dY'),             m = f (A = H)
-__global__ __launch_bounds__(kThreads) void dw_kernel(DwArgs a)
+template <class S>
+__global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
 {
-    using T0 = Tile<true, true, kWM, kWN, kGM, kGN, kNS>;
-    __shared__ __align__(16) uint8_t sm[smem_for<kWM>(T0::SMEM)];
+    __shared__ __align__(16) uint8_t sm[smem_for<S, S::WM>(S::template smem<true, true, S::WM>())];
     const uint32_t first = a.tiles_f2 * a.tiles_d, tiles = first + a.tiles_e * a.tiles_h;
     uint32_t part, ti;
     {
@@ -378,12 +573,12 @@ __global__ __launch_bounds__(kThreads) void dw_kernel(DwArgs a)
     const bool down = ti >= first;
     int64_t n0, m0;
     if (!down) {
-        n0 = (int64_t)(ti / a.tiles_d) * kBN;
-        m0 = (int64_t)(ti % a.tiles_d) * kBM;
+        n0 = (int64_t)(ti / a.tiles_d) * S::BN;
+        m0 = (int64_t)(ti % a.tiles_d) * S::BM;
     } else {
         ti -= first;
-        m0 = (int64_t)(ti / a.tiles_e) * kBM;
-        n0 = (int64_t)(ti % a.tiles_e) * kBN;
+        m0 = (int64_t)(ti / a.tiles_e) * S::BM;
+        n0 = (int64_t)(ti % a.tiles_e) * S::BN;
     }
     const int64_t nk = (a.T + kBK - 1) / kBK, k0 = part * nk / a.parts * kBK, k1 = (part + 1) * nk / a.parts * kBK;
     const int64_t ls = 3 * a.Fp, valid = (a.T < k1 ? a.T : k1) - k0;
@@ -391,16 +586,16 @@ __global__ __launch_bounds__(kThreads) void dw_kernel(DwArgs a)
                            : rows_of(a.X + k0 * kD, kD, m0, kD, valid);
     const Operand B = down ? rows_of(a.dY + k0 * kD, kD, n0, kD, valid)
                            : rows_of(a.S + k0 * ls, ls, n0, 2 * a.Fp, valid);
-    f32x16 acc[kWM][kWN];
+    f32x16 acc[S::WM][S::WN];
     clear(acc);
-    product<true, true, kWM, kWN, kGM, kGN, kNS>(A, B, k1 - k0, sm, acc);
-    const int w = threadIdx.x >> 6, wm = w / kGN, wn = w % kGN;
-    float *lds = reinterpret_cast<float *>(sm + w * Rows<kWM>::BYTES);
+    S::template run<true, true, S::WM>(A, B, 0, k1 - k0, sm, acc);
+    const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
+    float *lds = reinterpret_cast<float *>(sm + w * Rows<S::WM>::BYTES);
     float *pp = a.parts > 1 ? a.part + part * (3 * a.Fp * kD) : nullptr;
 #pragma unroll
-    for (int nb = 0; nb < kWN; ++nb) {
-        const int64_t nw = n0 + (wn * kWN + nb) * 32, mw = m0 + wm * 32 * kWM;
-        Rows<kWM>::write(
+    for (int nb = 0; nb < S::WN; ++nb) {
+        const int64_t nw = n0 + (wn * S::WN + nb) * 32, mw = m0 + wm * 32 * S::WM;
+        Rows<S::WM>::write(
             lds, [&](int mb, int e) { return acc[mb][nb][e]; },
             [&](int nn, int mm, float (&v)[8]) {
                 const int64_t n = nw + nn, m = mw + mm;
@@ -435,13 +630,7 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(DwArgs a)
     if (which == 2)
         at = 2 * a.Fp * kD + i / a.F * a.Fp + i % a.F;
     float v[8] = {};
-    for (int p = 0; p < a.parts; ++p) {
-        float x[8];
-        load_as(a.part + p * (3 * a.Fp * kD), true, at, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] += x[e];
-    }
+    add_parts(a.part, 3 * a.Fp * kD, a.parts, at, v);
     put_dw(a, which == 0 ? a.dWg : which == 1 ? a.dWu : a.dWd, i, which == 2 ? a.scale : 1.0f, v);
 }
 
@@ -469,6 +658,108 @@ struct Layout {
     uint64_t S, dY, part, total;
 };
 
+// ---- which tile, and how many parts of k
+//
+// Time of a launch in us, besides 2.5 that all have: turns(blocks) x (step x
+// steps of 64 k + rest), and for parts their sums' way through memory and the
+// launch that adds them.  turns(): a block alone on its CU is bound by latency,
+// a second one fits beside it for a third more, and from about five on the
+// CU's load path (see mfma_tile.hpp) makes them add up.  The constants are
+// measured (T = 30 ... 49,152, F = 1000 ... 4096, warm, one process):
+//   a step of rows: Half 0.45, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
+//   up (12 steps and epilogue): Half 4.2, Small 7.75, Square 23 us a block;
+//   grad (24 steps and epilogue): Half 8.6, Small 14.5, Wide 34 us a block.
+// E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 19 us (Half / Small / Square), T =
+// 49,152: Small 371, Square 276 us; grad at T = 100: 11.4 / 15.3 us (Half /
+// Small), T = 49,152: Small 628, Wide 565 us; down at T = 49,152: Small 167,
+// Mid 146 us; dW at T = 1024: Small 19.5, Square 28 us, at T = 49,152: Small
+// 532 (7 parts), Square 451 us (7 parts) against 1,132 (1 part).
+constexpr double kReduce = 3.0, kBytesPerUs = 4.5e6;
+constexpr int kMaxRowParts = 16;   // of a [T][768] result
+
+double rounds(int64_t blocks) { return (double)((blocks + kCUs - 1) / kCUs); }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+double turns(int64_t blocks)
+{
+    static const double few[] = {1.0, 1.0, 1.3, 2.0, 2.9};
+    const int64_t r = (blocks + kCUs - 1) / kCUs;
+    return r < 5 ? few[r] : 0.93 * (double)r;
+}
+
+struct Choice {
+    int shape, parts;   // index into the candidates
+    double us;
+};
+
+void consider(Choice &best, int shape, int parts, double us)
+{
+    if (best.parts == 0 || us < best.us)
+        best = Choice{shape, parts, us};
+}
+
+// 0 Half, 1 Small, 2 Square
+Choice choose_up(int64_t T, int64_t F)
+{
+    Choice c{};
+    consider(c, 0, 1, 4.2 * rounds(ceil_div(T, Half::BN) * ceil_div(F, Half::BM / 2)));
+    consider(c, 1, 1, 7.75 * rounds(ceil_div(T, Small::BN) * ceil_div(F, Small::BM / 2)));
+    consider(c, 2, 1, 23.0 * rounds(ceil_div(T, Square::BN) * ceil_div(F, Square::BM / 2)));
+    return c;
+}
+
+// 0 Half, 1 Small, 2 Wide
+Choice choose_grad(int64_t T, int64_t F)
+{
+    Choice c{};
+    consider(c, 0, 1, 8.6 * rounds(ceil_div(T, Half::BN) * ceil_div(F, Half::BM / 2)));
+    consider(c, 1, 1, 14.5 * rounds(ceil_div(T, Small::BN) * ceil_div(F, Small::BM / 2)));
+    consider(c, 2, 1, 34.0 * rounds(ceil_div(T, Wide::BN) * ceil_div(F, Wide::BM / 2)));
+    return c;
+}
+
+// A [T][768] result over `steps` stages of k; 0 Half, 1 Small, 2 Mid.  A part
+// has at least two stages, and parts only where a round of blocks holds them.
+Choice choose_rows(int64_t T, int64_t steps)
+{
+    Choice c{};
+    for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
+        const double add = p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0;
+        const double n = (double)ceil_div(steps, p);
+        const int64_t half = ceil_div(T, Half::BN) * (kD / Half::BM) * p, small = ceil_div(T, Small::BN) * (kD / Small::BM) * p;
+        if (p == 1 || half <= 2 * kCUs)
+            consider(c, 0, p, turns(half) * (0.45 * n + 2.0) + add);
+        if (p == 1 || small <= 2 * kCUs)
+            consider(c, 1, p, turns(small) * (0.62 * n + 2.0) + add);
+        if (p == 1)
+            consider(c, 2, p, turns(ceil_div(T, Mid::BN) * (kD / Mid::BM)) * (0.80 * n + 2.0));
+    }
+    return c;
+}
+
+// The most bytes the parts' sums take for any T up to max_tokens: with parts a
+// result has at most 2 kCUs blocks of 128 x 128.
+uint64_t row_part_bytes(int64_t max_tokens)
+{
+    const uint64_t all = 2ull * kCUs * Small::BM * Small::BN * 4, few = 4ull * kMaxRowParts * max_tokens * kD;
+    return all < few ? all : few;
+}
+
+// The weights' gradients; 0 Small, 1 Square.
+Choice choose_dw(int64_t T, int64_t F, int64_t Fp)
+{
+    Choice c{};
+    const int64_t steps = ceil_div(T, kBK);
+    for (int p = 1; p <= kMaxParts && p <= steps; ++p) {
+        const double add = p > 1 ? kReduce + p * Fp * (2.0 * 4 * 3 * kD) / kBytesPerUs : 0.0, n = (double)ceil_div(steps, p);
+        auto tiles = [&](int bm, int bn) { return (ceil_div(2 * Fp, bn) * (kD / bm) + (kD / bn) * ceil_div(F, bm)) * p; };
+        consider(c, 0, p, rounds(tiles(Small::BM, Small::BN)) * (0.47 * n + 1.3) + add);
+        consider(c, 1, p, rounds(tiles(Square::BM, Square::BN)) * (1.47 * n + 3.5) + add);
+    }
+    return c;
+}
+
 Layout layout(const ffn_config *c, int pass)
 {
     Layout L{};
@@ -482,8 +773,9 @@ Layout layout(const ffn_config *c, int pass)
     L.S = take(2ull * c->max_tokens * L.Fp * (pass == FFN_PASS_BWD ? 3 : 1));
     if (pass == FFN_PASS_BWD) {
         L.dY = take(2ull * c->max_tokens * kD);
-        L.part = take(4ull * kMaxParts * 3 * L.Fp * kD);
     }
+    const uint64_t rows = row_part_bytes(c->max_tokens), dw = 4ull * kMaxParts * 3 * L.Fp * kD;
+    L.part = take(pass == FFN_PASS_BWD && dw > rows ? dw : rows);
     L.total = o;
     return L;
 }
@@ -521,11 +813,84 @@ drop::Mask no_drop()
     return m;
 }
 
-// Share of the resident slots busy over all rounds of nb blocks.
-double round_fill(uint32_t nb, uint32_t slots)
+template <class S>
+void launch_up(Args a, int act, hipStream_t s)
 {
-    const uint32_t rounds = (nb + slots - 1) / slots;
-    return rounds ? (double)nb / ((double)rounds * slots) : 1.0;
+    a.tiles_t = blocks(a.T, S::BN);
+    a.tiles_o = blocks(a.F, S::BM / 2);
+    auto k = act == FFN_ACT_SILU ? up_kernel<S, FFN_ACT_SILU>
+             : act == FFN_ACT_GELU ? up_kernel<S, FFN_ACT_GELU> : up_kernel<S, FFN_ACT_RELU2>;
+    k<<<grid_blocks(a.tiles_t * a.tiles_o), S::THREADS, 0, s>>>(a);
+}
+
+template <class S, bool DX>
+void launch_rows(Args a, int parts, hipStream_t s)
+{
+    a.tiles_t = blocks(a.T, S::BN);
+    a.tiles_o = kD / S::BM;
+    a.parts = parts;
+    rows_kernel<S, DX><<<grid_blocks(a.tiles_t * a.tiles_o * (uint32_t)parts), S::THREADS, 0, s>>>(a);
+    if (parts > 1)
+        rows_reduce_kernel<DX><<<blocks(a.T * kD, 8 * 256), 256, 0, s>>>(a);
+}
+
+template <int NT>
+void launch_few(const Args &a, int act, hipStream_t s)
+{
+    auto k = act == FFN_ACT_SILU ? up_few_kernel<FFN_ACT_SILU, NT>
+             : act == FFN_ACT_GELU ? up_few_kernel<FFN_ACT_GELU, NT> : up_few_kernel<FFN_ACT_RELU2, NT>;
+    k<<<blocks(a.F, 16), 64 * kFewWaves, 0, s>>>(a);
+    down_few_kernel<NT><<<kD / 16, 64 * kFewDown, 0, s>>>(a);
+}
+
+template <class S>
+void launch_grad(Args a, int act, hipStream_t s)
+{
+    a.tiles_t = blocks(a.T, S::BN);
+    a.tiles_o = blocks(a.F, S::BM / 2);
+    auto k = act == FFN_ACT_SILU ? grad_kernel<S, FFN_ACT_SILU>
+             : act == FFN_ACT_GELU ? grad_kernel<S, FFN_ACT_GELU> : grad_kernel<S, FFN_ACT_RELU2>;
+    k<<<grid_blocks(a.tiles_t * a.tiles_o), S::THREADS, 0, s>>>(a);
+}
+
+// The weights' gradients.
+template <class S>
+void launch_dw(DwArgs d, int parts, hipStream_t s)
+{
+    d.tiles_f2 = blocks(2 * d.Fp, S::BN);
+    d.tiles_d = kD / S::BM;
+    d.tiles_e = kD / S::BN;
+    d.tiles_h = blocks(d.F, S::BM);
+    const uint32_t tiles = d.tiles_f2 * d.tiles_d + d.tiles_e * d.tiles_h;
+    d.parts = parts;
+    dw_kernel<S><<<grid_blocks(tiles * (uint32_t)parts), S::THREADS, 0, s>>>(d);
+    if (parts > 1)
+        dw_reduce_kernel<<<dim3(blocks(d.F * kD, 8 * 256), 3), 256, 0, s>>>(d);
+}
+
+void up(const Args &a, int act, hipStream_t s)
+{
+    const Choice c = choose_up(a.T, a.F);
+    (c.shape == 0 ? launch_up<Half> : c.shape == 1 ? launch_up<Small> : launch_up<Square>)(a, act, s);
+}
+
+void grad(const Args &a, int act, hipStream_t s)
+{
+    const Choice c = choose_grad(a.T, a.F);
+    (c.shape == 0 ? launch_grad<Half> : c.shape == 1 ? launch_grad<Small> : launch_grad<Wide>)(a, act, s);
+}
+
+template <bool DX>
+void rows(const Args &a, hipStream_t s)
+{
+    const Choice c = choose_rows(a.T, (DX ? 2 : 1) * a.Fp / kBK);
+    (c.shape == 0 ? launch_rows<Half, DX> : c.shape == 1 ? launch_rows<Small, DX> : launch_rows<Mid, DX>)(a, c.parts, s);
+}
+
+void dw(const DwArgs &d, hipStream_t s)
+{
+    const Choice c = choose_dw(d.T, d.F, d.Fp);
+    (c.shape == 0 ? launch_dw<Small> : launch_dw<Square>)(d, c.parts, s);
 }
 
 }   // namespace
@@ -631,6 +996,7 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.Wu = (const uint16_t *)Wu;
     a.Wd = (const uint16_t *)Wd;
     a.S = (uint16_t *)((uint8_t *)ws + L.S);
+    a.part = (float *)((uint8_t *)ws + L.part);
     a.T = T;
     a.F = cfg->hidden;
     a.Fp = L.Fp;
@@ -639,13 +1005,16 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.out = Y;
     a.out_f32 = cfg->y_dtype == FFN_DTYPE_F32;
     hipStream_t s = (hipStream_t)stream;
-    a.tiles_t = blocks(T, kBN);
-    a.tiles_o = blocks(a.F, kBM / 2);
-    auto up = cfg->act == FFN_ACT_SILU ? up_kernel<FFN_ACT_SILU>
-              : cfg->act == FFN_ACT_GELU ? up_kernel<FFN_ACT_GELU> : up_kernel<FFN_ACT_RELU2>;
-    up<<<grid_blocks(a.tiles_t * a.tiles_o), kThreads, 0, s>>>(a);
-    a.tiles_o = kD / kBM;
-    rows_kernel<false><<<grid_blocks(a.tiles_t * a.tiles_o), kThreads, 0, s>>>(a);
+    if (T > kFewRows) {
+        up(a, cfg->act, s);
+        rows<false>(a, s);
+    } else if (T > 32) {
+        launch_few<4>(a, cfg->act, s);
+    } else if (T > 16) {
+        launch_few<2>(a, cfg->act, s);
+    } else {
+        launch_few<1>(a, cfg->act, s);
+    }
     return done();
 }
 
@@ -687,6 +1056,7 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.Wd = (const uint16_t *)Wd;
     a.dY = (const uint16_t *)dY;
     a.S = (uint16_t *)((uint8_t *)ws + L.S);
+    a.part = (float *)((uint8_t *)ws + L.part);
     a.T = T;
     a.F = cfg->hidden;
     a.Fp = L.Fp;
@@ -699,40 +1069,14 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
         dy_kernel<<<blocks(groups, 256), 256, 0, s>>>(dY, a.out_f32, a.mask, groups, m);
         a.dY = m;
     }
-    a.tiles_t = blocks(T, kBN);
-    a.tiles_o = blocks(a.F, kBM / 2);
-    auto grad = cfg->act == FFN_ACT_SILU ? grad_kernel<FFN_ACT_SILU>
-                : cfg->act == FFN_ACT_GELU ? grad_kernel<FFN_ACT_GELU> : grad_kernel<FFN_ACT_RELU2>;
-    grad<<<grid_blocks(a.tiles_t * a.tiles_o), kThreads, 0, s>>>(a);
-    a.tiles_o = kD / kBM;
-    rows_kernel<true><<<grid_blocks(a.tiles_t * a.tiles_o), kThreads, 0, s>>>(a);
-
     d.X = a.X;
     d.dY = a.dY;
     d.S = a.S;
     d.scale = a.mask.scale;
-    d.tiles_f2 = blocks(2 * d.Fp, kBN);
-    d.tiles_d = kD / kBM;
-    d.tiles_e = kD / kBN;
-    d.tiles_h = blocks(d.F, kBM);
-    const uint32_t tiles = d.tiles_f2 * d.tiles_d + d.tiles_e * d.tiles_h;
-    // parts of k by the fill of the rounds of resident blocks (two per CU);
-    // parts cost their reduction, about 3 %
-    int parts = 1;
-    double best = 0.0;
-    const int64_t nk = blocks(T, kBK);
-    for (int p = 1; p <= kMaxParts && p <= nk; ++p) {
-        const double score = round_fill(tiles * p, 2 * kCUs) * (p > 1 ? 0.97 : 1.0);
-        if (score > best + 1e-9) {
-            best = score;
-            parts = p;
-        }
-    }
-    d.parts = parts;
     d.part = (float *)((uint8_t *)ws + L.part);
-    dw_kernel<<<grid_blocks(tiles * (uint32_t)parts), kThreads, 0, s>>>(d);
-    if (parts > 1)
-        dw_reduce_kernel<<<rgrid, 256, 0, s>>>(d);
+    grad(a, cfg->act, s);
+    rows<true>(a, s);
+    dw(d, s);
     return done();
 }
 

@@ -136,7 +136,7 @@ def fwd(s: DropSpec, x: torch.Tensor, residual: torch.Tensor | None = None, out:
     dx, dy = _dtype(x.dtype, "x"), _dtype(yt, "the result")
     pr = None if residual is None else _marshal.ptr(residual, "residual", dev, yt, x.shape)
     if out is None:
-        out = torch.empty(x.shape, dtype=yt, device=dev)
+        out = torch.empty_like(x, dtype=yt)
     _check_rng(s, dev)
     rc = _marshal.enqueue(lib().drop_fwd, dev, s, px, dx, pr, _marshal.ptr(out, "out", dev, yt, x.shape), dy, rows, cols)
     if rc:
@@ -154,7 +154,7 @@ def bwd(s: DropSpec, dy: torch.Tensor, out: torch.Tensor | None = None,
     py = _marshal.ptr(dy, "dy", dev)
     ty, tx = _dtype(dy.dtype, "dy"), _dtype(xt, "the result")
     if out is None:
-        out = torch.empty(dy.shape, dtype=xt, device=dev)
+        out = torch.empty_like(dy, dtype=xt)
     _check_rng(s, dev)
     rc = _marshal.enqueue(lib().drop_bwd, dev, s, py, ty, _marshal.ptr(out, "out", dev, xt, dy.shape), tx, rows, cols)
     if rc:
