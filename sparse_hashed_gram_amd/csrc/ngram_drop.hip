@@ -2,12 +2,16 @@
 //   out[i][j] = k[i][j] c (s_b W_b[r_b(i)][j] + s_t W_t[r_t(i)][j]),
 // k and c the mask and scale of include/drop.h for a [T][768] tensor.
 //
-// The sweep is the plain forward's: a block hashes 64 positions into LDS, then
-// all its threads walk the 64 x 96 groups of 8 elements, consecutive lanes on
-// consecutive pieces of a row.  A thread holds a whole mask group, so it makes
-// one Philox call for the 48 (bf16) or 96 (fp32) bytes its group moves: bound
-// by HBM and cache bandwidth like the plain forward, with no second pass that
-// reads and writes the output again.
+// The sweep is the plain forward's: a block hashes its positions into LDS, then
+// its threads take the positions' 96 groups of 8 elements each, consecutive
+// lanes on consecutive pieces of a row.  A thread holds whole mask groups, so it
+// makes one Philox call for the 48 (bf16) or 96 (fp32) bytes a group moves:
+// bound by HBM and cache bandwidth like the plain forward, with no second pass
+// that reads and writes the output again.  8 positions per block, three groups
+// per thread, all their loads in flight: 34.3 us for 49,152 positions of 16 GB
+// of bf16 tables (6.6 TB/s of rows and output, Zipf rows partly from the
+// caches) against 36.0 us with 64 positions per block, and 10.3 against 14.6 us
+// for 2,048 positions, which then are 256 blocks instead of 32.
 #include "ngram_dev.hpp"
 #include "philox.hpp"
 
@@ -17,7 +21,7 @@ namespace ngram {
 
 namespace {
 
-constexpr int kTok = 64;
+constexpr int kTok = 8;   // positions per block
 constexpr int kThreads = 256;
 constexpr int kGroups = kDim / 8;   // mask groups of a row
 
@@ -41,14 +45,13 @@ __device__ __forceinline__ Piece<ELT> load_piece(const uint8_t *table, uint32_t 
 }
 
 template <int ELT>
-__device__ __forceinline__ void widen(const Piece<ELT> &a, float sign, float (&v)[8])
+__device__ __forceinline__ void widen(const Piece<ELT> &a, uint32_t sign, float (&v)[8])
 {
-    const uint32_t f = sign < 0.0f ? 0x80000000u : 0u;
     const uint32_t *u = reinterpret_cast<const uint32_t *>(a.w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t x = ELT == 2 ? ((k & 1) ? u[k / 2] & 0xFFFF0000u : u[k / 2] << 16) : u[k];
-        v[k] = __uint_as_float(x ^ f);
+        v[k] = __uint_as_float(x ^ sign);
     }
 }
 
@@ -60,45 +63,46 @@ __global__ __launch_bounds__(kThreads) void fwd_drop_kernel(const int32_t *__res
                                                             const uint8_t *__restrict__ wt, drop::Mask mask,
                                                             uint8_t *__restrict__ out, uint32_t *__restrict__ flags)
 {
-    constexpr int kIter = kTok * kGroups / kThreads;   // 24
-    constexpr int kU = ELT == 2 ? 4 : 2;               // groups in flight per thread
-    static_assert(kIter % kU == 0, "unroll must divide the sweep");
+    constexpr int kIter = kTok * kGroups / kThreads;   // 3, all in flight
+    static_assert(kTok * kGroups % kThreads == 0 && kTok <= kThreads, "whole sweeps");
     __shared__ uint32_t s_idx[2][kTok];
     const int tid = threadIdx.x;
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    if (tid < kTok) {
-        uint32_t ib = 0, it = 0;
-        const int64_t i = t0 + tid;
-        if (i < T && ngram_index(tok, i, hp, ib, it) && flags)
-            atomicOr(flags, NGRAM_FLAG_BAD_TOKEN);
-        s_idx[0][tid] = ib;
-        s_idx[1][tid] = it;
-    }
-    __syncthreads();
-    const int ntok = (int)min<int64_t>(kTok, T - t0);
     const drop::Key key = drop::key_of(mask);
-#pragma unroll 1
-    for (int g = 0; g < kIter; g += kU) {
-        Piece<ELT> a[kU], b[kU];
+    for (int64_t t0 = (int64_t)blockIdx.x * kTok; t0 < T; t0 += (int64_t)gridDim.x * kTok) {
+        if (tid < kTok) {
+            uint32_t ib = 0, it = 0;
+            const int64_t i = t0 + tid;
+            if (i < T && ngram_index(tok, i, hp, ib, it) && flags)
+                atomicOr(flags, NGRAM_FLAG_BAD_TOKEN);
+            s_idx[0][tid] = ib;
+            s_idx[1][tid] = it;
+        }
+        __syncthreads();
+        const int ntok = (int)min<int64_t>(kTok, T - t0);
+        Piece<ELT> a[kIter], b[kIter];
+        uint32_t sa[kIter], sb[kIter];   // sign bits
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int e = tid + (g + u) * kThreads, lt = e / kGroups, c = e - lt * kGroups;
+        for (int u = 0; u < kIter; ++u) {
+            const int e = tid + u * kThreads, lt = e / kGroups, c = e - lt * kGroups;
             if (lt < ntok) {
-                a[u] = load_piece<ELT>(wb, s_idx[0][lt] & 0x7FFFFFFFu, c);
+                const uint32_t ib = s_idx[0][lt], it = s_idx[1][lt];
+                sa[u] = ib & 0x80000000u;
+                sb[u] = it & 0x80000000u;
+                a[u] = load_piece<ELT>(wb, ib & 0x7FFFFFFFu, c);
                 if (!DIRECT)
-                    b[u] = load_piece<ELT>(wt, s_idx[1][lt] & 0x7FFFFFFFu, c);
+                    b[u] = load_piece<ELT>(wt, it & 0x7FFFFFFFu, c);
             }
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int e = tid + (g + u) * kThreads, lt = e / kGroups;
+        for (int u = 0; u < kIter; ++u) {
+            const int e = tid + u * kThreads, lt = e / kGroups;
             if (lt >= ntok)
                 continue;
             float v[8];
-            widen<ELT>(a[u], (s_idx[0][lt] >> 31) ? -1.0f : 1.0f, v);
+            widen<ELT>(a[u], sa[u], v);
             if (!DIRECT) {
                 float x[8];
-                widen<ELT>(b[u], (s_idx[1][lt] >> 31) ? -1.0f : 1.0f, x);
+                widen<ELT>(b[u], sb[u], x);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     v[k] += x[k];
@@ -119,6 +123,7 @@ __global__ __launch_bounds__(kThreads) void fwd_drop_kernel(const int32_t *__res
                 st_global_nt<float4>(o + 16, make_float4(v[4], v[5], v[6], v[7]));
             }
         }
+        __syncthreads();   // s_idx is the next turn's
     }
 }
 
@@ -130,7 +135,8 @@ hipError_t launch_fwd_drop(int dtype, bool out_f32, const HashParams &hp, const 
 {
     if (T == 0)
         return hipSuccess;
-    const unsigned g = (unsigned)((T + kTok - 1) / kTok);
+    // a launch counts its threads in 32 bits: a longer micro-step takes several turns of the grid
+    const unsigned g = (unsigned)min((T + kTok - 1) / kTok, int64_t(1) << 23);
     auto k = dtype == NGRAM_DTYPE_BF16 ? (out_f32 ? fwd_drop_kernel<2, 4, false> : fwd_drop_kernel<2, 2, false>)
                                        : fwd_drop_kernel<4, 4, false>;
     if (hp.direct)

@@ -205,6 +205,20 @@ def test_embedding_with_dropout(T, dtype, out_f32, direct):
     assert torch.equal(got, d.fwd(s, full, out_dtype=got.dtype))
 
 
+def test_embedding_longer_than_one_launch_of_blocks():
+    # more positions than the grid's blocks hold at once (8 each, 2^23 blocks)
+    n, d = N(), D()
+    T = (1 << 26) + 77
+    cfg = n.config(300, 7, (300, 1), "bf16", max_tokens=T, direct=True)
+    W = _tables(1, "bf16", (300,))[0]
+    tok = torch.randint(0, 300, (T,), dtype=torch.int32, device="cuda")
+    got = n.embed_fwd_drop(cfg, W, None, tok, d.spec(0.5, 8, 9))
+    for lo in (0, (1 << 26) - 40, T - 50):
+        k = torch.from_numpy(orc.keep_rows(np.arange(lo, lo + 50), 768, 0.5, 8, 9)).cuda()
+        want = torch.where(k, 2.0 * W[tok[lo:lo + 50].long()].float(), 0.0)
+        assert torch.equal(got[lo:lo + 50].float(), want), lo
+
+
 def test_embedding_without_dropout_is_the_plain_forward():
     n, d = N(), D()
     cfg = n.config(300, 7, (211, 389), "bf16", max_tokens=200)
