@@ -41,12 +41,13 @@ constexpr uint32_t kGroup = 8;
 
 __host__ __device__ inline uint32_t grid_blocks(uint32_t tiles) { return kXcds * ((tiles + kXcds - 1) / kXcds); }
 
-// rows: tiles of positions, cols: tiles of the other side
-__device__ inline bool tile_of(uint32_t rows, uint32_t cols, uint32_t &rt, uint32_t &ct)
+// rows: tiles of positions, cols: tiles of the other side; block: the block's
+// number, blockIdx.x or, where a block takes several tiles, that plus turns of the grid
+__device__ inline bool tile_of(uint32_t block, uint32_t rows, uint32_t cols, uint32_t &rt, uint32_t &ct)
 {
     const uint32_t total = rows * cols, per = (total + kXcds - 1) / kXcds;
-    const uint32_t t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-    if (blockIdx.x / kXcds >= per || t >= total)
+    const uint32_t t = (block % kXcds) * per + block / kXcds;
+    if (block / kXcds >= per || t >= total)
         return false;
     const uint32_t span = kGroup * cols, g = t / span, first = g * kGroup;
     const uint32_t gm = rows - first < kGroup ? rows - first : kGroup;
@@ -88,6 +89,37 @@ struct Rows {
             const float4 a = *(const float4 *)(lds + n * LD + m), b = *(const float4 *)(lds + n * LD + m + 4);
             float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             out(n, m, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
+// The same for values that leave as bf16, in 4 KB of LDS per wavefront: rows of
+// 64 bf16, 8 chunks of 16 bytes, chunk c of row n at c ^ (n & 7).  out(n, m, w)
+// takes 8 consecutive m of one n, packed.
+struct RowsBf16 {
+    static constexpr uint32_t BYTES = 4096;
+
+    template <typename V, typename O>
+    static __device__ __forceinline__ void write(uint8_t *lds, V val, O out)
+    {
+        const int lane = fresh_tid() & 63, n = lane & 31;
+        uint8_t *p = lds + n * 128 + 8 * (lane >> 5);
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint2 w;
+                w.x = ngram::bf16_pack_rne(val(mb, 4 * q), val(mb, 4 * q + 1));
+                w.y = ngram::bf16_pack_rne(val(mb, 4 * q + 2), val(mb, 4 * q + 3));
+                *(uint2 *)(p + 16 * ((4 * mb + q) ^ (n & 7))) = w;
+                __builtin_amdgcn_sched_barrier(0);   // few values in flight: the accumulators leave few registers
+            }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + lane / 8, c = lane % 8;
+            out(r, 8 * c, *(const uint4 *)(lds + r * 128 + 16 * (c ^ (r & 7))));
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -188,7 +220,6 @@ struct Shape {
 using Half = Shape<2, 1, 2, 2>;     // 128 x 64, 4 wavefronts, three blocks per CU
 using Small = Shape<2, 2, 2, 2>;    // 128 x 128, 4 wavefronts, two blocks per CU
 using Mid = Shape<2, 3, 2, 2>;      // 128 x 192, 4 wavefronts, two blocks per CU (81,920 bytes of LDS each)
-using Wide = Shape<2, 3, 4, 2>;     // 256 x 192, 8 wavefronts
 using Square = Shape<4, 2, 2, 4>;   // 256 x 256, 8 wavefronts
 
 struct Args {
@@ -226,7 +257,7 @@ __global__ __launch_bounds__(S::THREADS) void up_kernel(Args a)
     constexpr int HB = S::WM / 2;
     __shared__ __align__(16) uint8_t sm[smem_for<S, HB>(S::template smem<false, false, S::WM>())];
     uint32_t tt, ot;
-    if (!tile_of(a.tiles_t, a.tiles_o, tt, ot))
+    if (!tile_of(blockIdx.x, a.tiles_t, a.tiles_o, tt, ot))
         return;
     const int64_t n0 = (int64_t)tt * S::BN, f0 = (int64_t)ot * (S::BM / 2);
     f32x16 acc[S::WM][S::WN];
@@ -280,7 +311,7 @@ __global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
 {
     __shared__ __align__(16) uint8_t sm[smem_for<S, S::WM>(S::template smem<DX, false, S::WM>())];
     uint32_t tt, ot;
-    if (!tile_of(a.tiles_t, a.tiles_o * (uint32_t)a.parts, tt, ot))
+    if (!tile_of(blockIdx.x, a.tiles_t, a.tiles_o * (uint32_t)a.parts, tt, ot))
         return;
     const uint32_t part = ot / a.tiles_o;
     ot -= part * a.tiles_o;
@@ -357,7 +388,7 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
     __shared__ __align__(16) uint8_t sm[smem_for<S, HB>(
         cmax(S::template smem<false, false, S::WM>(), S::template smem<true, false, HB>()))];
     uint32_t tt, ot;
-    if (!tile_of(a.tiles_t, a.tiles_o, tt, ot))
+    if (!tile_of(blockIdx.x, a.tiles_t, a.tiles_o, tt, ot))
         return;
     const int64_t n0 = (int64_t)tt * S::BN, f0 = (int64_t)ot * (S::BM / 2);
     f32x16 acc[S::WM][S::WN], dh[HB][S::WN];
@@ -394,6 +425,179 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
             put(2));
         Rows<HB>::write(lds, [&](int mb, int e) { return acc[mb][nb][e]; }, put(1));
         Rows<HB>::write(lds, [&](int mb, int e) { return acc[mb + HB][nb][e]; }, put(0));
+    }
+}
+
+// ------------------------------------------- many tiles on eight wavefronts
+//
+// up_kernel and grad_kernel on Square tiles, one block per CU that takes tiles
+// in turns.  With 12 steps of k a tile, what is around the steps counts: while
+// a product's last step runs, the first stage of the next product (dH's, or the
+// next tile's) is loaded already, and a tile's results leave through LDS of
+// their own (the two stages and 8 x 4 KB make up the CU's 160 KB) while the
+// next tile begins.  One launch of a block per tile measured 277 us for H of
+// 49,152 x 2048 and 580 us for the gradients (on 256 x 192 tiles; 600 with
+// spills on 256 x 256); this 263 us (1.18 PFLOP/s) and 503 us (0.92 PFLOP/s),
+// of which storing 604 MB is about 80 us.  Storing H between the two products
+// (fewer bytes at a time) cost more registers than there are: 625 us.
+constexpr int kLds = 160 * 1024;
+
+using G8 = Square;
+using LX = Loader<false, G8::BN, G8::NW>;        // rows of X and of dY'
+using LW = Loader<false, G8::BM, G8::NW>;        // rows of Wg and Wu, in turns of 64
+using LD = Loader<true, G8::BM / 2, G8::NW>;     // columns of Wd
+using FX = Reader<false, G8::BN, G8::WN>;
+using FW = Reader<false, G8::BM, G8::WM>;
+using FD = Reader<true, G8::BM / 2, G8::WM / 2>;
+constexpr uint32_t kStage8 = LX::BYTES + LW::BYTES;
+static_assert(2 * kStage8 + G8::NW * RowsBf16::BYTES == kLds && G8::WM == 4 && LD::BYTES <= LW::BYTES, "the CU's LDS");
+
+// A product's operands: the position side, which the two products share, and the weights'.
+template <class LA, class FA, int WM>
+struct View {
+    LA &la;
+    LX &lb;
+    const FA &ra;
+    const FX &rb;
+
+    __device__ __forceinline__ void issue(lds_u8 *stage)
+    {
+        lb.issue(stage);
+        la.issue(stage + LX::BYTES);
+    }
+
+    __device__ __forceinline__ void read(const lds_u8 *stage, int kk, bf16x8 (&x)[WM], bf16x8 (&y)[G8::WN]) const
+    {
+#pragma unroll
+        for (int mb = 0; mb < WM; ++mb)
+            x[mb] = ra.get(stage, mb, kk);
+#pragma unroll
+        for (int nb = 0; nb < G8::WN; ++nb)
+            y[nb] = rb.get(stage, nb, kk);
+    }
+};
+
+// A tile's first position and unit, moved back where it would reach past the
+// last: every tile is whole, so the lanes' offsets never change and the next
+// tile costs scalar work only.  (Needs T and F of at least a tile.  What two
+// tiles share, both compute and write, bit for bit the same.)
+struct TileAt {
+    int64_t n0, f0;
+    bool ok;
+};
+
+__device__ __forceinline__ TileAt next_tile(const Args &a, uint32_t block)
+{
+    TileAt p;
+    uint32_t tt = 0, ot = 0;
+    p.ok = tile_of(block, a.tiles_t, a.tiles_o, tt, ot);
+    p.n0 = min((int64_t)tt * G8::BN, a.T - G8::BN);
+    p.f0 = min((int64_t)ot * (G8::BM / 2), a.F - G8::BM / 2);
+    return p;
+}
+
+__device__ __forceinline__ Operand gate_up(const Args &a, const TileAt &p)
+{
+    return Operand{{a.Wg, a.Wu}, kD, p.f0, a.F, INT32_MAX, kD, 16 * G8::WM};
+}
+
+__device__ __forceinline__ Operand positions(const Args &a, const uint16_t *src, const TileAt &p)
+{
+    return rows_of(src, kD, p.n0, a.T, kD);
+}
+
+// BWD false: H; true: dG, dU and H.
+template <int ACT, bool BWD>
+__global__ __launch_bounds__(G8::THREADS) void hidden8_kernel(Args a)
+{
+    __shared__ __align__(16) uint8_t sm[kLds];
+    uint32_t block = blockIdx.x;
+    TileAt p = next_tile(a, block);
+    if (!p.ok)
+        return;
+    lds_u8 *s0, *s1;
+    places(sm, kStage8, s0, s1);
+    const int w = wave_id(), wm = w / G8::GN, wn = w % G8::GN;
+    LX lx;
+    LW lw;
+    LD ld;
+    FX fx;
+    FW fw;
+    FD fd;
+    lx.set_lanes(positions(a, a.X, p));
+    lw.set_lanes(gate_up(a, p));
+    fx.init(0, wn * 32 * G8::WN);
+    fw.init(LX::BYTES, wm * 32 * G8::WM);
+    if constexpr (BWD) {
+        ld.set_lanes(rows_of(a.Wd, a.F, p.f0, a.F, kD));
+        fd.init(LX::BYTES, wm * 16 * G8::WM);
+    }
+    View<LW, FW, G8::WM> gu{lw, lx, fw, fx};
+    View<LD, FD, G8::WM / 2> du{ld, lx, fd, fx};
+    auto begin = [&](const TileAt &q, lds_u8 *stage) {
+        lx.set_base(positions(a, a.X, q), 0);
+        lw.set_base(gate_up(a, q), 0);
+        gu.issue(stage);
+    };
+    begin(p, s0);
+    wait_vmcnt<0>();
+    barrier_nofence();
+    uint8_t *lds = sm + 2 * kStage8 + w * RowsBf16::BYTES;
+    while (p.ok) {
+        f32x16 acc[G8::WM][G8::WN], dh[G8::WM / 2][G8::WN];
+        clear(acc);
+        block += gridDim.x;
+        const TileAt q = next_tile(a, block);
+        chain8(gu, kD / kBK, s0, s1, acc, [&](lds_u8 *stage) {
+            if constexpr (BWD) {
+                lx.set_base(positions(a, a.dY, p), 0);
+                ld.set_base(rows_of(a.Wd, a.F, p.f0, a.F, kD), 0);
+                du.issue(stage);
+            } else if (q.ok) {
+                begin(q, stage);
+            }
+        });
+        if constexpr (BWD) {
+            clear(dh);
+            chain8(du, kD / kBK, s0, s1, dh, [&](lds_u8 *stage) {
+                if (q.ok)
+                    begin(q, stage);
+            });
+        }
+        const int64_t ls = (BWD ? 3 : 1) * a.Fp;
+        uint16_t *const at = a.S + (p.n0 + wn * 32 * G8::WN) * ls + p.f0 + wm * 64;
+#pragma unroll
+        for (int nb = 0; nb < G8::WN; ++nb) {
+            auto put = [&](int64_t which) {
+                return [&, which](int n, int m, const uint4 &v) {
+                    *reinterpret_cast<uint4 *>(at + (32 * nb + n) * ls + which * a.Fp + m) = v;
+                };
+            };
+            if constexpr (BWD) {
+                RowsBf16::write(
+                    lds,
+                    [&](int mb, int e) {
+                        const float g = acc[mb][nb][e], up = acc[mb + 2][nb][e], h = a.mask.scale * dh[mb][nb][e];
+                        float d;
+                        const float s = act<ACT, true>(g, d);
+                        acc[mb][nb][e] = h * s;
+                        acc[mb + 2][nb][e] = h * up * d;
+                        return s * up;
+                    },
+                    put(2));
+                RowsBf16::write(lds, [&](int mb, int e) { return acc[mb][nb][e]; }, put(1));
+                RowsBf16::write(lds, [&](int mb, int e) { return acc[mb + 2][nb][e]; }, put(0));
+            } else {
+                RowsBf16::write(
+                    lds,
+                    [&](int mb, int e) {
+                        float d;
+                        return act<ACT, false>(acc[mb][nb][e], d) * acc[mb + 2][nb][e];
+                    },
+                    put(0));
+            }
+        }
+        p = q;
     }
 }
 
@@ -667,11 +871,11 @@ struct Layout {
 // CU's load path (see mfma_tile.hpp) makes them add up.  The constants are
 // measured (T = 30 ... 49,152, F = 1000 ... 4096, warm, one process):
 //   a step of rows: Half 0.45, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
-//   up (12 steps and epilogue): Half 4.2, Small 7.75, Square 23 us a block;
-//   grad (24 steps and epilogue): Half 8.6, Small 14.5, Wide 34 us a block.
-// E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 19 us (Half / Small / Square), T =
-// 49,152: Small 371, Square 276 us; grad at T = 100: 11.4 / 15.3 us (Half /
-// Small), T = 49,152: Small 628, Wide 565 us; down at T = 49,152: Small 167,
+//   up (12 steps and epilogue): Half 4.2, Small 7.75, hidden8 22 us a block;
+//   grad (24 steps and epilogue): Half 8.6, Small 14.5, hidden8 40 us a block.
+// E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 24 us (Half / Small / hidden8), T =
+// 49,152: Small 371, hidden8 263 us; grad at T = 100: 11.4 / 15.3 us (Half /
+// Small), T = 49,152: Small 620, hidden8 503 us; down at T = 49,152: Small 167,
 // Mid 146 us; dW at T = 1024: Small 19.5, Square 28 us, at T = 49,152: Small
 // 532 (7 parts), Square 451 us (7 parts) against 1,132 (1 part).
 constexpr double kReduce = 3.0, kBytesPerUs = 4.5e6;
@@ -699,23 +903,15 @@ void consider(Choice &best, int shape, int parts, double us)
         best = Choice{shape, parts, us};
 }
 
-// 0 Half, 1 Small, 2 Square
-Choice choose_up(int64_t T, int64_t F)
+// Tiles of positions x units; 0 Half, 1 Small, 2 hidden8_kernel's.
+Choice choose_hidden(int64_t T, int64_t F, bool bwd)
 {
     Choice c{};
-    consider(c, 0, 1, 4.2 * rounds(ceil_div(T, Half::BN) * ceil_div(F, Half::BM / 2)));
-    consider(c, 1, 1, 7.75 * rounds(ceil_div(T, Small::BN) * ceil_div(F, Small::BM / 2)));
-    consider(c, 2, 1, 23.0 * rounds(ceil_div(T, Square::BN) * ceil_div(F, Square::BM / 2)));
-    return c;
-}
-
-// 0 Half, 1 Small, 2 Wide
-Choice choose_grad(int64_t T, int64_t F)
-{
-    Choice c{};
-    consider(c, 0, 1, 8.6 * rounds(ceil_div(T, Half::BN) * ceil_div(F, Half::BM / 2)));
-    consider(c, 1, 1, 14.5 * rounds(ceil_div(T, Small::BN) * ceil_div(F, Small::BM / 2)));
-    consider(c, 2, 1, 34.0 * rounds(ceil_div(T, Wide::BN) * ceil_div(F, Wide::BM / 2)));
+    auto tiles = [&](int bn, int bm) { return ceil_div(T, bn) * ceil_div(F, bm / 2); };
+    consider(c, 0, 1, (bwd ? 8.6 : 4.2) * rounds(tiles(Half::BN, Half::BM)));
+    consider(c, 1, 1, (bwd ? 14.5 : 7.75) * rounds(tiles(Small::BN, Small::BM)));
+    if (T >= G8::BN && F >= G8::BM / 2)
+        consider(c, 2, 1, (bwd ? 40.0 : 22.0) * rounds(tiles(G8::BN, G8::BM)));
     return c;
 }
 
@@ -823,6 +1019,18 @@ void launch_up(Args a, int act, hipStream_t s)
     k<<<grid_blocks(a.tiles_t * a.tiles_o), S::THREADS, 0, s>>>(a);
 }
 
+// T of at least G8::BN, F of at least G8::BM / 2
+template <bool BWD>
+void launch_hidden8(Args a, int act, hipStream_t s)
+{
+    a.tiles_t = blocks(a.T, G8::BN);
+    a.tiles_o = blocks(a.F, G8::BM / 2);
+    const uint32_t n = grid_blocks(a.tiles_t * a.tiles_o);
+    auto k = act == FFN_ACT_SILU ? hidden8_kernel<FFN_ACT_SILU, BWD>
+             : act == FFN_ACT_GELU ? hidden8_kernel<FFN_ACT_GELU, BWD> : hidden8_kernel<FFN_ACT_RELU2, BWD>;
+    k<<<n < kCUs ? n : kCUs, G8::THREADS, 0, s>>>(a);
+}
+
 template <class S, bool DX>
 void launch_rows(Args a, int parts, hipStream_t s)
 {
@@ -870,14 +1078,14 @@ void launch_dw(DwArgs d, int parts, hipStream_t s)
 
 void up(const Args &a, int act, hipStream_t s)
 {
-    const Choice c = choose_up(a.T, a.F);
-    (c.shape == 0 ? launch_up<Half> : c.shape == 1 ? launch_up<Small> : launch_up<Square>)(a, act, s);
+    const Choice c = choose_hidden(a.T, a.F, false);
+    (c.shape == 0 ? launch_up<Half> : c.shape == 1 ? launch_up<Small> : launch_hidden8<false>)(a, act, s);
 }
 
 void grad(const Args &a, int act, hipStream_t s)
 {
-    const Choice c = choose_grad(a.T, a.F);
-    (c.shape == 0 ? launch_grad<Half> : c.shape == 1 ? launch_grad<Small> : launch_grad<Wide>)(a, act, s);
+    const Choice c = choose_hidden(a.T, a.F, true);
+    (c.shape == 0 ? launch_grad<Half> : c.shape == 1 ? launch_grad<Small> : launch_hidden8<true>)(a, act, s);
 }
 
 template <bool DX>

@@ -53,6 +53,15 @@ __device__ __forceinline__ void barrier_nofence()
     asm volatile("" ::: "memory");
 }
 
+// threadIdx.x, worked out anew where it is used: what is derived from it is not
+// kept in registers from one place to the next.
+__device__ __forceinline__ int fresh_tid()
+{
+    int t = (int)threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // One operand of a contraction.  Rows past the last and columns past the last
@@ -105,17 +114,15 @@ struct Loader {
         ch = KMAJ ? pos ^ (4 * (r & 3) & (CH - 1)) : pos ^ ((r >> 1) & 7);
     }
 
-    // k0: the first stage's first k, a multiple of kBK
-    __device__ __forceinline__ void init(const Operand &o, int32_t k0)
+    // The lanes' offsets.  They hold for every tile that lies inside the operand.
+    __device__ __forceinline__ void set_lanes(const Operand &o)
     {
-        k = k0;
-        seg = o.seg;
-        k_valid = o.k_valid;
         w = wave_id();
+        const int tid = fresh_tid();
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             int r, ch;
-            place((int)threadIdx.x, j, r, ch);
+            place(tid, j, r, ch);
             second[j] = false;
             if constexpr (KMAJ) {
                 const int64_t c = o.first + 8 * ch < o.count ? 8 * ch : 0;
@@ -131,6 +138,14 @@ struct Loader {
                 off[j] = (uint32_t)(2 * (i * o.ld + 8 * ch));
             }
         }
+    }
+
+    // The first stage: k0, a multiple of kBK.  Scalar work only.
+    __device__ __forceinline__ void set_base(const Operand &o, int32_t k0)
+    {
+        k = k0;
+        seg = o.seg;
+        k_valid = o.k_valid;
         const int64_t at = KMAJ ? o.first : o.first * o.ld;
         step = 2 * (KMAJ ? kBK * o.ld : kBK);
         next_src = (const uint8_t *)(o.src[1] + at);
@@ -154,8 +169,7 @@ struct Loader {
                 load((!KMAJ && second[j] ? cur[1] : cur[0]) + o, lds, j);
             }
         } else {
-            int tid = (int)threadIdx.x;
-            asm volatile("" : "+v"(tid));   // rare: worked out here, not kept in registers over the loop
+            const int tid = fresh_tid();   // rare
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 int r, ch;
@@ -191,7 +205,7 @@ struct Reader {
     // at: the operand's bytes into a stage
     __device__ __forceinline__ void init(uint32_t at, int row0)
     {
-        const int lane = threadIdx.x & 63;
+        const int lane = fresh_tid() & 63;
         if constexpr (KMAJ) {
             // within each 16 lanes, lane p addresses row p / 4, columns 4 (p % 4) .. of the
             // four k rows, and receives rows 0 .. 3 of column p.  row0 is a multiple of the
@@ -244,16 +258,18 @@ struct Tile {
     __device__ __forceinline__ void init(const Operand &A, const Operand &B, int32_t k0)
     {
         const int w = wave_id();
-        la.init(A, k0);
-        lb.init(B, k0);
-        ra.init(0, w / GN * 32 * WM);
-        rb.init(LA::BYTES, w % GN * 32 * WN);
+        la.set_lanes(A);
+        la.set_base(A, k0);
+        lb.set_lanes(B);
+        lb.set_base(B, k0);
+        ra.init(LB::BYTES, w / GN * 32 * WM);
+        rb.init(0, w % GN * 32 * WN);
     }
 
     __device__ __forceinline__ void issue(lds_u8 *stage)
     {
-        la.issue(stage);
-        lb.issue(stage + LA::BYTES);
+        lb.issue(stage);
+        la.issue(stage + LB::BYTES);
     }
 
     __device__ __forceinline__ void read(const lds_u8 *stage, int kk, bf16x8 (&a)[WM], bf16x8 (&b)[WN]) const
@@ -364,16 +380,15 @@ __device__ __forceinline__ void products8(const bf16x8 (&fa)[2][WM], const bf16x
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// One stage of a group, with the start of the next one if there is one.
-template <int GROUP, bool AK, bool BK, int WM, int WN, int GM, int GN>
-__device__ __forceinline__ void step8(Tile<AK, BK, WM, WN, GM, GN> &t, bool more, const lds_u8 *__restrict__ stage,
-                                      lds_u8 *__restrict__ other, f32x16 (&acc)[WM][WN])
+// One stage of a group; next(other) starts what follows it, if anything.
+template <int GROUP, typename T, int WM, int WN, typename Next>
+__device__ __forceinline__ void step8(T &t, const lds_u8 *__restrict__ stage,
+                                      lds_u8 *__restrict__ other, f32x16 (&acc)[WM][WN], Next next)
 {
     bf16x8 fa[2][WM], fb[2][WN];
     t.read(stage, 0, fa[0], fb[0]);
     t.read(stage, 1, fa[1], fb[1]);
-    if (more)
-        t.issue(other);
+    next(other);
     barrier_nofence();
     products8(fa, fb, acc);
     barrier_nofence();
@@ -388,20 +403,48 @@ __device__ __forceinline__ void step8(Tile<AK, BK, WM, WN, GM, GN> &t, bool more
     barrier_nofence();
 }
 
-template <int GROUP, bool AK, bool BK, int WM, int WN, int GM, int GN>
-__device__ __forceinline__ void loop8(Tile<AK, BK, WM, WN, GM, GN> &t, int nk, lds_u8 *s0, lds_u8 *s1,
-                                      f32x16 (&acc)[WM][WN])
+template <int GROUP, typename T, int WM, int WN, typename Next>
+__device__ __forceinline__ void loop8(T &t, int nk, lds_u8 *&s0, lds_u8 *&s1,
+                                      f32x16 (&acc)[WM][WN], Next next)
 {
     if (GROUP == 1)
         barrier_nofence();
     for (int H = 0; H < nk; ++H) {
-        step8<GROUP>(t, H + 1 < nk, s0, s1, acc);
+        step8<GROUP>(t, s0, s1, acc, [&](lds_u8 *other) {
+            if (H + 1 < nk)
+                t.issue(other);
+            else
+                next(other);
+        });
         lds_u8 *const other = s0;
         s0 = s1;
         s1 = other;
     }
     if (GROUP == 0)
         barrier_nofence();
+}
+
+// acc += the product over nk stages of t (a Tile, or its like: issue, read), whose first stage lies in s0, landed
+// for every wavefront.  next(stage) starts the first stage of whatever is
+// multiplied after it (or nothing): afterwards that lies in s0, landed for every
+// wavefront, and s1 is free.
+template <typename T, int WM, int WN, typename Next>
+__device__ __forceinline__ void chain8(T &t, int nk, lds_u8 *&s0, lds_u8 *&s1, f32x16 (&acc)[WM][WN], Next next)
+{
+    if (wave_id() < 4)
+        loop8<0>(t, nk, s0, s1, acc, next);
+    else
+        loop8<1>(t, nk, s0, s1, acc, next);
+}
+
+// The two stages' places.  The second as a value, not a constant: past the 64 KB
+// that an LDS read's offset reaches, folded constants would cost a register per
+// read.
+__device__ __forceinline__ void places(uint8_t *sm, uint32_t stage, lds_u8 *&s0, lds_u8 *&s1)
+{
+    asm volatile("" : "+s"(stage));
+    s0 = (lds_u8 *)sm;
+    s1 = s0 + stage;
 }
 
 // acc += the product over K values of k from k0 on (both multiples of kBK, K at
@@ -414,20 +457,14 @@ __device__ __forceinline__ void product(const Operand &A, const Operand &B, int3
     static_assert(GM * GN <= 4 || GM * GN == 8, "one group, or two of four");
     T t;
     t.init(A, B, k0);
-    // the second stage's place as a value, not a constant: past the 64 KB that an
-    // LDS read's offset reaches, folded constants would cost a register per read
-    uint32_t second = T::STAGE;
-    asm volatile("" : "+s"(second));
-    lds_u8 *s0 = (lds_u8 *)sm, *s1 = s0 + second;
+    lds_u8 *s0, *s1;
+    places(sm, T::STAGE, s0, s1);
     const int nk = K / kBK;
     t.issue(s0);
     if constexpr (GM * GN == 8) {
         wait_vmcnt<0>();
         barrier_nofence();
-        if (wave_id() < 4)
-            loop8<0>(t, nk, s0, s1, acc);
-        else
-            loop8<1>(t, nk, s0, s1, acc);
+        chain8(t, nk, s0, s1, acc, [](lds_u8 *) {});
     } else {
         if (nk > 1) {
             t.issue(s1);
