@@ -307,11 +307,13 @@ __device__ __forceinline__ void put_rows(const Args &a, const drop::Key &key, in
 // A [T][768] result: DX false: Y = (res +) drop(H Wd^T); true: dX = [dG | dU] [Wg; Wu].
 // With parts of k, each block's sums go to the workspace and rows_reduce_kernel ends the pass.
 template <class S, bool DX>
-__global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
+constexpr uint32_t kRowsLds = smem_for<S, S::WM>(S::template smem<DX, false, S::WM>());
+
+template <class S, bool DX>
+__device__ __forceinline__ void rows_tile(const Args &a, uint32_t block, uint8_t *sm)
 {
-    __shared__ __align__(16) uint8_t sm[smem_for<S, S::WM>(S::template smem<DX, false, S::WM>())];
     uint32_t tt, ot;
-    if (!tile_of(blockIdx.x, a.tiles_t, a.tiles_o * (uint32_t)a.parts, tt, ot))
+    if (!tile_of(block, a.tiles_t, a.tiles_o * (uint32_t)a.parts, tt, ot))
         return;
     const uint32_t part = ot / a.tiles_o;
     ot -= part * a.tiles_o;
@@ -346,6 +348,13 @@ __global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
                     put_rows<DX>(a, key, i, v);
             });
     }
+}
+
+template <class S, bool DX>
+__global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
+{
+    __shared__ __align__(16) uint8_t sm[kRowsLds<S, DX>];
+    rows_tile<S, DX>(a, blockIdx.x, sm);
 }
 
 // v += the parts' 8 values at i, in order; four parts' loads at a time are in flight.
@@ -603,11 +612,16 @@ __global__ __launch_bounds__(G8::THREADS) void hidden8_kernel(Args a)
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 64 positions: the weights' bytes bound the pass, and the latency of
+// Up to 32 positions: the weights' bytes bound the pass, and the latency of
 // one round of loads most of it.  No LDS stages and no k loop over barriers:
 // every wavefront loads its share of k straight into matrix-core fragments
 // (16 weight rows x 16 positions x 32 values of k each), all loads in flight at
-// once, and the wavefronts' sums meet in LDS.
+// once, and the wavefronts' sums meet in LDS.  F = 2048: T = 1 7.9 us against
+// 14.5 through the tiles, T = 16 10 against 15, T = 32 12.7 against 15.5.  The
+// down product has 48 blocks whatever F, so F and T F are bounded: the two
+// meet near T F = 96 Ki (16 x 6144 19 against 19 us, 24 x 4096 16 against 16,
+// 32 x 4096 18 against 16) and, for one position, between F = 8192 (16.5
+// against 20) and 16,384 (29 against 26).
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
@@ -615,8 +629,13 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-constexpr int kFewWaves = 4, kFewRows = 64;
+constexpr int kFewWaves = 4;
 constexpr int kFewDown = 8;   // wavefronts of a down block
+
+bool few_rows(int64_t T, int64_t F)
+{
+    return T <= 32 && F <= 8192 && T * F <= 96 * 1024;
+}
 
 // H of 16 hidden units, NT tiles of 16 positions; a wavefront takes a quarter of k.
 template <int ACT, int NT>
@@ -760,16 +779,18 @@ __device__ __forceinline__ void put_dw(const DwArgs &a, void *dst, int64_t i, fl
 //   dWg | dWu: n = f of 2 Fp (B = dG | dU), m = d (A = X)
 //   dWd:       n = d (B = dY'),             m = f (A = H)
 template <class S>
-__global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
+constexpr uint32_t kDwLds = smem_for<S, S::WM>(S::template smem<true, true, S::WM>());
+
+template <class S>
+__device__ __forceinline__ void dw_tile(const DwArgs &a, uint32_t block, uint8_t *sm)
 {
-    __shared__ __align__(16) uint8_t sm[smem_for<S, S::WM>(S::template smem<true, true, S::WM>())];
     const uint32_t first = a.tiles_f2 * a.tiles_d, tiles = first + a.tiles_e * a.tiles_h;
     uint32_t part, ti;
     {
         // parts outermost: the blocks that run together share their rows of k
         const uint32_t total = tiles * (uint32_t)a.parts, per = (total + kXcds - 1) / kXcds;
-        const uint32_t t = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-        if (blockIdx.x / kXcds >= per || t >= total)
+        const uint32_t t = (block % kXcds) * per + block / kXcds;
+        if (block / kXcds >= per || t >= total)
             return;
         part = t / tiles;
         ti = t % tiles;
@@ -820,6 +841,27 @@ __global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
                 }
             });
     }
+}
+
+template <class S>
+__global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
+{
+    __shared__ __align__(16) uint8_t sm[kDwLds<S>];
+    dw_tile<S>(a, blockIdx.x, sm);
+}
+
+// dX and the weights' gradients in one launch: neither needs the other, and
+// alone neither fills the chip while a backward is short (T = 257, F = 1000: 12.0
+// us against 11.6 + 8.6, T = 4096, F = 2048: 73 against 44 + 67).
+template <class S>
+__global__ __launch_bounds__(S::THREADS) void tail_kernel(Args a, DwArgs d, uint32_t row_blocks)
+{
+    static_assert(S::THREADS == Small::THREADS, "one block size");
+    __shared__ __align__(16) uint8_t sm[cmax(kRowsLds<S, true>, kDwLds<Small>)];
+    if (blockIdx.x < row_blocks)
+        rows_tile<S, true>(a, blockIdx.x, sm);
+    else
+        dw_tile<Small>(d, blockIdx.x - row_blocks, sm);
 }
 
 // The parts of k, added in order; blockIdx.y: dWg, dWu, dWd.  parts = 0 gives
@@ -915,6 +957,12 @@ Choice choose_hidden(int64_t T, int64_t F, bool bwd)
     return c;
 }
 
+// Tiles of the three weights' gradients.
+int64_t dw_tiles(int64_t F, int64_t Fp, int bm, int bn)
+{
+    return ceil_div(2 * Fp, bn) * (kD / bm) + (kD / bn) * ceil_div(F, bm);
+}
+
 // A [T][768] result over `steps` stages of k; 0 Half, 1 Small, 2 Mid.  A part
 // has at least two stages, and parts only where a round of blocks holds them.
 Choice choose_rows(int64_t T, int64_t steps)
@@ -934,6 +982,28 @@ Choice choose_rows(int64_t T, int64_t steps)
     return c;
 }
 
+// dX and the weights' gradients in one launch, dX on Half or Small tiles:
+// blocks of two lengths, so their mean counts where there are more than CUs.
+Choice choose_tail(int64_t T, int64_t F, int64_t Fp)
+{
+    Choice c{};
+    const int64_t steps = 2 * Fp / kBK;
+    const double dn = (double)dw_tiles(F, Fp, Small::BM, Small::BN), dt = 0.47 * ceil_div(T, kBK) + 1.3;
+    auto one = [&](int shape, int p, int64_t n, double t) {
+        const int64_t all = n * p + (int64_t)dn;
+        const double longest = t > dt ? t : dt, mean = (n * p * t + dn * dt) / all, r = rounds(all);
+        const double us = r <= 1.0 ? 1.2 * longest : (1.1 * r * mean > longest ? 1.1 * r * mean : longest);
+        if (p == 1 || n * p <= 2 * (int64_t)kCUs)
+            consider(c, shape, p, us + (p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0));
+    };
+    for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
+        const double n = (double)ceil_div(steps, p);
+        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.45 * n + 2.0);
+        one(1, p, ceil_div(T, Small::BN) * (kD / Small::BM), 0.62 * n + 2.0);
+    }
+    return c;
+}
+
 // The most bytes the parts' sums take for any T up to max_tokens: with parts a
 // result has at most 2 kCUs blocks of 128 x 128.
 uint64_t row_part_bytes(int64_t max_tokens)
@@ -949,9 +1019,8 @@ Choice choose_dw(int64_t T, int64_t F, int64_t Fp)
     const int64_t steps = ceil_div(T, kBK);
     for (int p = 1; p <= kMaxParts && p <= steps; ++p) {
         const double add = p > 1 ? kReduce + p * Fp * (2.0 * 4 * 3 * kD) / kBytesPerUs : 0.0, n = (double)ceil_div(steps, p);
-        auto tiles = [&](int bm, int bn) { return (ceil_div(2 * Fp, bn) * (kD / bm) + (kD / bn) * ceil_div(F, bm)) * p; };
-        consider(c, 0, p, rounds(tiles(Small::BM, Small::BN)) * (0.47 * n + 1.3) + add);
-        consider(c, 1, p, rounds(tiles(Square::BM, Square::BN)) * (1.47 * n + 3.5) + add);
+        consider(c, 0, p, rounds(p * dw_tiles(F, Fp, Small::BM, Small::BN)) * (0.47 * n + 1.3) + add);
+        consider(c, 1, p, rounds(p * dw_tiles(F, Fp, Square::BM, Square::BN)) * (1.47 * n + 3.5) + add);
     }
     return c;
 }
@@ -1031,15 +1100,29 @@ void launch_hidden8(Args a, int act, hipStream_t s)
     k<<<n < kCUs ? n : kCUs, G8::THREADS, 0, s>>>(a);
 }
 
-template <class S, bool DX>
-void launch_rows(Args a, int parts, hipStream_t s)
+// a with the tiles and parts of a [T][768] result; its blocks
+template <class S>
+uint32_t set_rows(Args &a, int parts)
 {
     a.tiles_t = blocks(a.T, S::BN);
     a.tiles_o = kD / S::BM;
     a.parts = parts;
-    rows_kernel<S, DX><<<grid_blocks(a.tiles_t * a.tiles_o * (uint32_t)parts), S::THREADS, 0, s>>>(a);
-    if (parts > 1)
+    return grid_blocks(a.tiles_t * a.tiles_o * (uint32_t)parts);
+}
+
+template <bool DX>
+void reduce_rows(const Args &a, hipStream_t s)
+{
+    if (a.parts > 1)
         rows_reduce_kernel<DX><<<blocks(a.T * kD, 8 * 256), 256, 0, s>>>(a);
+}
+
+template <class S, bool DX>
+void launch_rows(Args a, int parts, hipStream_t s)
+{
+    const uint32_t n = set_rows<S>(a, parts);
+    rows_kernel<S, DX><<<n, S::THREADS, 0, s>>>(a);
+    reduce_rows<DX>(a, s);
 }
 
 template <int NT>
@@ -1061,19 +1144,39 @@ void launch_grad(Args a, int act, hipStream_t s)
     k<<<grid_blocks(a.tiles_t * a.tiles_o), S::THREADS, 0, s>>>(a);
 }
 
-// The weights' gradients.
+// The same for the weights' gradients.
 template <class S>
-void launch_dw(DwArgs d, int parts, hipStream_t s)
+uint32_t set_dw(DwArgs &d, int parts)
 {
     d.tiles_f2 = blocks(2 * d.Fp, S::BN);
     d.tiles_d = kD / S::BM;
     d.tiles_e = kD / S::BN;
     d.tiles_h = blocks(d.F, S::BM);
-    const uint32_t tiles = d.tiles_f2 * d.tiles_d + d.tiles_e * d.tiles_h;
     d.parts = parts;
-    dw_kernel<S><<<grid_blocks(tiles * (uint32_t)parts), S::THREADS, 0, s>>>(d);
-    if (parts > 1)
+    return grid_blocks((d.tiles_f2 * d.tiles_d + d.tiles_e * d.tiles_h) * (uint32_t)parts);
+}
+
+void reduce_dw(const DwArgs &d, hipStream_t s)
+{
+    if (d.parts > 1)
         dw_reduce_kernel<<<dim3(blocks(d.F * kD, 8 * 256), 3), 256, 0, s>>>(d);
+}
+
+template <class S>
+void launch_dw(DwArgs d, int parts, hipStream_t s)
+{
+    const uint32_t n = set_dw<S>(d, parts);
+    dw_kernel<S><<<n, S::THREADS, 0, s>>>(d);
+    reduce_dw(d, s);
+}
+
+// (with parts of the weights' gradients both sums would lie in one place)
+template <class S>
+void launch_tail(Args a, int parts, DwArgs d, hipStream_t s)
+{
+    const uint32_t n = set_rows<S>(a, parts), m = set_dw<Small>(d, 1);
+    tail_kernel<S><<<n + m, S::THREADS, 0, s>>>(a, d, n);
+    reduce_rows<true>(a, s);
 }
 
 void up(const Args &a, int act, hipStream_t s)
@@ -1095,10 +1198,16 @@ void rows(const Args &a, hipStream_t s)
     (c.shape == 0 ? launch_rows<Half, DX> : c.shape == 1 ? launch_rows<Small, DX> : launch_rows<Mid, DX>)(a, c.parts, s);
 }
 
-void dw(const DwArgs &d, hipStream_t s)
+// dX and the weights' gradients
+void tail(const Args &a, const DwArgs &d, hipStream_t s)
 {
-    const Choice c = choose_dw(d.T, d.F, d.Fp);
-    (c.shape == 0 ? launch_dw<Small> : launch_dw<Square>)(d, c.parts, s);
+    const Choice both = choose_tail(a.T, a.F, a.Fp), x = choose_rows(a.T, 2 * a.Fp / kBK), w = choose_dw(a.T, a.F, a.Fp);
+    if (both.us < x.us + w.us + 2.5) {
+        (both.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, both.parts, d, s);
+        return;
+    }
+    rows<true>(a, s);
+    (w.shape == 0 ? launch_dw<Small> : launch_dw<Square>)(d, w.parts, s);
 }
 
 }   // namespace
@@ -1213,11 +1322,9 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.out = Y;
     a.out_f32 = cfg->y_dtype == FFN_DTYPE_F32;
     hipStream_t s = (hipStream_t)stream;
-    if (T > kFewRows) {
+    if (!few_rows(T, a.F)) {
         up(a, cfg->act, s);
         rows<false>(a, s);
-    } else if (T > 32) {
-        launch_few<4>(a, cfg->act, s);
     } else if (T > 16) {
         launch_few<2>(a, cfg->act, s);
     } else {
@@ -1283,8 +1390,7 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     d.scale = a.mask.scale;
     d.part = (float *)((uint8_t *)ws + L.part);
     grad(a, cfg->act, s);
-    rows<true>(a, s);
-    dw(d, s);
+    tail(a, d, s);
     return done();
 }
 

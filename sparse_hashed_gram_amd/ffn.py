@@ -166,7 +166,7 @@ def fwd(cfg: FfnConfig, ws: Workspace, X: torch.Tensor, Wg: torch.Tensor, Wu: to
     pg, pu, pd = _weights(cfg, Wg, Wu, Wd, dev, torch.bfloat16)
     pr = None if residual is None else _marshal.ptr(residual, "residual", dev, cfg.y_torch_dtype, (T, DIM))
     if out is None:
-        out = torch.empty((T, DIM), dtype=cfg.y_torch_dtype, device=dev)
+        out = torch.empty_like(X, dtype=cfg.y_torch_dtype)
     _check("ffn_fwd", _marshal.enqueue(lib().ffn_fwd, dev, cfg, ws.ptr, ws.nbytes, px, pg, pu, pd, pr, drop, T,
                                        _marshal.ptr(out, "out", dev, cfg.y_torch_dtype, (T, DIM))))
     return out
@@ -188,13 +188,13 @@ def bwd(cfg: FfnConfig, ws: Workspace, X: torch.Tensor, Wg: torch.Tensor, Wu: to
     if cfg.options & OPT_ACCUM and (dWg is None or dWu is None or dWd is None):
         raise ValueError("an accumulating backward needs the gradients it adds to: dWg, dWu, dWd")
     if dX is None:
-        dX = torch.empty((T, DIM), dtype=cfg.y_torch_dtype, device=dev)
+        dX = torch.empty_like(dY)
     if dWg is None:
-        dWg = torch.empty((cfg.hidden, DIM), dtype=wt, device=dev)
+        dWg = torch.empty_like(Wg, dtype=wt)
     if dWu is None:
-        dWu = torch.empty((cfg.hidden, DIM), dtype=wt, device=dev)
+        dWu = torch.empty_like(Wu, dtype=wt)
     if dWd is None:
-        dWd = torch.empty((DIM, cfg.hidden), dtype=wt, device=dev)
+        dWd = torch.empty_like(Wd, dtype=wt)
     _check("ffn_bwd", _marshal.enqueue(
         lib().ffn_bwd, dev, cfg, ws.ptr, ws.nbytes, px, pg, pu, pd, py, drop, T,
         _marshal.ptr(dX, "dX", dev, cfg.y_torch_dtype, (T, DIM)), *_weights(cfg, dWg, dWu, dWd, dev, wt, "d")))
