@@ -10,26 +10,28 @@ import torch
 # the stream's handle without the object around it (2 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def ptr(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None) -> int:
     """The address of a contiguous GPU tensor on `device`, after the checks."""
+    if (t.is_cuda and t.device == device and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def enqueue(f, device: torch.device, *args) -> int:
     """f(*args, stream) on the device's current stream; its status."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _device():
         return f(*args, _raw_stream(device.index))
     with torch.cuda.device(device):
         return f(*args, _raw_stream(device.index))

@@ -20,6 +20,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "li
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+_U64 = 1 << 64
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
@@ -85,7 +86,7 @@ def rng_state(seed: int, offset: int, out: torch.Tensor | None = None, device="c
 
 def _signed(v: int) -> int:
     v = int(v)
-    if not 0 <= v < 1 << 64:
+    if not 0 <= v < _U64:
         raise ValueError("seed and offset are 64-bit unsigned numbers")
     return v - (1 << 64) if v >> 63 else v
 
@@ -95,8 +96,10 @@ def spec(p: float, seed: int = 0, offset: int = 0, rng: torch.Tensor | None = No
     generator state in device memory (rng_state) that the kernels read when
     they run, so a captured graph replays with the mask of whatever it holds
     then.  Calls need offsets of their own, or they get the same mask."""
-    _signed(seed), _signed(offset)
-    s = DropSpec(p, 0, int(seed), int(offset), None)
+    seed, offset = int(seed), int(offset)
+    if not (0 <= seed < _U64 and 0 <= offset < _U64):
+        raise ValueError("seed and offset are 64-bit unsigned numbers")
+    s = DropSpec(p, 0, seed, offset, None)
     if rng is not None:
         if rng.dtype != torch.int64 or rng.numel() != 2:
             raise ValueError("rng must be an int64 [2] tensor")
@@ -137,8 +140,11 @@ def fwd(s: DropSpec, x: torch.Tensor, residual: torch.Tensor | None = None, out:
     pr = None if residual is None else _marshal.ptr(residual, "residual", dev, yt, x.shape)
     if out is None:
         out = torch.empty_like(x, dtype=yt)
+        po = out.data_ptr()
+    else:
+        po = _marshal.ptr(out, "out", dev, yt, x.shape)
     _check_rng(s, dev)
-    rc = _marshal.enqueue(lib().drop_fwd, dev, s, px, dx, pr, _marshal.ptr(out, "out", dev, yt, x.shape), dy, rows, cols)
+    rc = _marshal.enqueue(lib().drop_fwd, dev, s, px, dx, pr, po, dy, rows, cols)
     if rc:
         raise DropError("drop_fwd", rc)
     return out
@@ -155,8 +161,11 @@ def bwd(s: DropSpec, dy: torch.Tensor, out: torch.Tensor | None = None,
     ty, tx = _dtype(dy.dtype, "dy"), _dtype(xt, "the result")
     if out is None:
         out = torch.empty_like(dy, dtype=xt)
+        po = out.data_ptr()
+    else:
+        po = _marshal.ptr(out, "out", dev, xt, dy.shape)
     _check_rng(s, dev)
-    rc = _marshal.enqueue(lib().drop_bwd, dev, s, py, ty, _marshal.ptr(out, "out", dev, xt, dy.shape), tx, rows, cols)
+    rc = _marshal.enqueue(lib().drop_bwd, dev, s, py, ty, po, tx, rows, cols)
     if rc:
         raise DropError("drop_bwd", rc)
     return out

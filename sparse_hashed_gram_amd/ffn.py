@@ -167,8 +167,10 @@ def fwd(cfg: FfnConfig, ws: Workspace, X: torch.Tensor, Wg: torch.Tensor, Wu: to
     pr = None if residual is None else _marshal.ptr(residual, "residual", dev, cfg.y_torch_dtype, (T, DIM))
     if out is None:
         out = torch.empty_like(X, dtype=cfg.y_torch_dtype)
-    _check("ffn_fwd", _marshal.enqueue(lib().ffn_fwd, dev, cfg, ws.ptr, ws.nbytes, px, pg, pu, pd, pr, drop, T,
-                                       _marshal.ptr(out, "out", dev, cfg.y_torch_dtype, (T, DIM))))
+        po = out.data_ptr()
+    else:
+        po = _marshal.ptr(out, "out", dev, cfg.y_torch_dtype, (T, DIM))
+    _check("ffn_fwd", _marshal.enqueue(lib().ffn_fwd, dev, cfg, ws.ptr, ws.nbytes, px, pg, pu, pd, pr, drop, T, po))
     return out
 
 
