@@ -55,7 +55,8 @@ extern "C" {
 
 /* The generator's state in device memory (16 bytes, 16-byte aligned): read
  * by the kernels when they run, so a captured graph draws the mask of
- * whatever the caller stored there last. */
+ * whatever the caller stored there last.  It lies outside a call's results
+ * and workspace. */
 typedef struct drop_rng {
     uint64_t seed;
     uint64_t offset;

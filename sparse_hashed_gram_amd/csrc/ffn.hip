@@ -4,8 +4,12 @@
 //   up_kernel     H = a(X Wg^T) * (X Wu^T)                  -> workspace, bf16
 //   rows_kernel   Y = (res +) drop(H Wd^T); dX = dG Wg + dU Wu (one contraction over 2 F)
 //   grad_kernel   G, U again, dH = dY' Wd -> dG, dU, H       -> workspace, bf16
+//   hidden8_kernel  up_kernel's or grad_kernel's results on 256 x 256 tiles, for many positions
 //   dw_kernel     dWg, dWu, dWd in one launch, k = T, in parts where the tiles alone
 //                 do not fill the chip; dw_reduce_kernel adds the parts in order
+//   tail_kernel   dX and dWg, dWu, dWd in one launch, for few positions
+//   up_few_kernel, down_few_kernel  the forward of up to 32 positions
+//   dy_kernel     dY' where dY is fp32 or was dropped: a masked copy in bf16
 //
 // Every product is a block tile of mfma_tile.hpp.  Weights are read as they
 // lie: where k runs over a weight's rows (dH, dX) or over positions (the weights'
@@ -36,7 +40,9 @@ inline int64_t rup(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // The hardware hands consecutive workgroups to the 8 XCDs in turn.  Each XCD
 // gets a contiguous range of tiles, walked in groups of 8 tiles of positions
 // (all weight tiles of a group before the next group), so the blocks that are
-// resident on an XCD share their operands in its L2.
+// resident on an XCD share their operands in its L2.  49,152 x 2048, groups of 1 /
+// 4 / 8 / 16: H 293 / 257 / 257 / 259 us, gradients of the hidden units 543 / 500 /
+// 496 / 542, Y 151 / 149 / 141 / 144, dX 302 / 302 / 300 / 315.
 constexpr uint32_t kGroup = 8;
 
 __host__ __device__ inline uint32_t grid_blocks(uint32_t tiles) { return kXcds * ((tiles + kXcds - 1) / kXcds); }
@@ -306,6 +312,8 @@ __device__ __forceinline__ void put_rows(const Args &a, const drop::Key &key, in
 
 // A [T][768] result: DX false: Y = (res +) drop(H Wd^T); true: dX = [dG | dU] [Wg; Wu].
 // With parts of k, each block's sums go to the workspace and rows_reduce_kernel ends the pass.
+// 49,152 x 2048: Y 146 us (1.06 PFLOP/s), with dropout and a residual 176 us
+// (its 75 MB more, read or not 32 rows ahead: 174 us); dX 303 us (1.02 PFLOP/s).
 template <class S, bool DX>
 constexpr uint32_t kRowsLds = smem_for<S, S::WM>(S::template smem<DX, false, S::WM>());
 
@@ -775,7 +783,9 @@ __device__ __forceinline__ void put_dw(const DwArgs &a, void *dst, int64_t i, fl
     store_as(dst, a.dw_f32, i, v);
 }
 
-// One tile of one part of k: rows n of the result with m contiguous.
+// One tile of one part of k: rows n of the result with m contiguous.  Both
+// operands are k-major, so nothing is transposed in memory.  49,152 x 2048: 440 us in
+// 7 parts and 12 us to add them (1.05 PFLOP/s of products).
 //   dWg | dWu: n = f of 2 Fp (B = dG | dU), m = d (A = X)
 //   dWd:       n = d (B = dY'),             m = f (A = H)
 template <class S>
@@ -851,8 +861,9 @@ __global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
 }
 
 // dX and the weights' gradients in one launch: neither needs the other, and
-// alone neither fills the chip while a backward is short (T = 257, F = 1000: 12.0
-// us against 11.6 + 8.6, T = 4096, F = 2048: 73 against 44 + 67).
+// alone neither fills the chip while a backward is short (T = 257, F = 1000: 13.3
+// us against 19.4, T = 4096, F = 2048: 71 against 97; from about 6,000 x 2048 on
+// the larger tiles of dw_kernel win, 8,192 x 2304: 162 against 157).
 template <class S>
 __global__ __launch_bounds__(S::THREADS) void tail_kernel(Args a, DwArgs d, uint32_t row_blocks)
 {
@@ -880,7 +891,9 @@ __global__ __launch_bounds__(256) void dw_reduce_kernel(DwArgs a)
     put_dw(a, which == 0 ? a.dWg : which == 1 ? a.dWu : a.dWd, i, which == 2 ? a.scale : 1.0f, v);
 }
 
-// dY' as the products take it: bf16, dropped places 0, unscaled.
+// dY' as the products take it: bf16, dropped places 0, unscaled (49,152 rows of
+// bf16: 24 us, one pass over 151 MB; masking in the products' loads would need them
+// to pass through registers).
 __global__ __launch_bounds__(256) void dy_kernel(const void *dY, int f32, drop::Mask m, int64_t groups, uint16_t *out)
 {
     const drop::Key key = drop::key_of(m);
@@ -1292,6 +1305,12 @@ static int check_call(const ffn_config *cfg, int pass, void *ws, uint64_t ws_byt
             return FFN_EARG;
     if (meet(r, work) || (res && res != outs[0].p && meet(r, outs[0])))
         return FFN_EARG;
+    const Span rng{drop ? drop->rng : nullptr, sizeof(drop_rng)};
+    if (meet(rng, work))
+        return FFN_EARG;
+    for (int i = 0; i < n_out; ++i)
+        if (meet(rng, outs[i]))
+            return FFN_EARG;
     return FFN_OK;
 }
 

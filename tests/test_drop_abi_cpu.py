@@ -95,3 +95,15 @@ def test_embed_fwd_drop_rejects_as_embed_fwd_does(D):
     assert f(c, P, P, None, 0, s, None, None, None) == 0
     c.dim = 512
     assert f(c, P, P, P, 10, s, Q, None, None) == -3
+
+
+def test_generator_state_inside_the_results_is_refused(D):
+    # a block could write over the state before another has read it
+    from sparse_hashed_gram_amd import ngram as N
+    n = 10 * 768 * 4
+    for at in (Q, Q + n - 16):
+        r = D.DropSpec(0.5, 0, 1, 2, at)
+        assert D.lib().drop_fwd(r, P, 0, None, Q, 0, 10, 768, None) == -5
+        assert D.lib().drop_bwd(r, P, 0, Q, 0, 10, 768, None) == -5
+        c = N.config(50304, 50256, (4096, 4096), "f32", max_tokens=64)
+        assert N.lib().ngram_embed_fwd_drop(c, P, P, P, 10, r, Q, None, None) == -5

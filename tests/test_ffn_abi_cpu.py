@@ -113,3 +113,13 @@ def test_binding_refuses(F):
         F.fwd(c, ws, z(4, 768, dtype=torch.bfloat16), z(64, 768), z(64, 768), z(768, 64))
     with pytest.raises(ValueError, match="X must have shape"):
         F.fwd(c, ws, z(768, dtype=torch.bfloat16), z(64, 768), z(64, 768), z(768, 64))
+
+
+def test_generator_state_inside_results_or_workspace_is_refused(F):
+    from sparse_hashed_gram_amd import drop
+    c = F.config(64, 256)
+    n = F.workspace_bytes(c)
+    for at in (A[4], A[4] + 100 * 1536 - 16, WS + 512):
+        assert F.lib().ffn_fwd(c, WS, n, *A[:4], None, drop.DropSpec(0.5, 0, 0, 0, at), 100, A[4], None) == -5
+    for at in (A[5], A[6], A[7], A[8] + 64, WS + n - 16):
+        assert F.lib().ffn_bwd(c, WS, n, *A[:5], drop.DropSpec(0.5, 0, 0, 0, at), 100, *A[5:9], None) == -5

@@ -378,3 +378,28 @@ def test_refusals_on_the_gpu():
     with pytest.raises(m.FfnError) as e:
         m.fwd(cfg, ws, flat[4:].view(16, 768), *W)  # 8-byte aligned
     assert e.value.status == -2
+
+
+def test_offsets_past_32_bits():
+    # H has 2.2e9 elements, dG | dU | H three times as many (12.9 GB): exact, as
+    # above, on the first and last positions; dY is 0 on all others, so the
+    # weights' gradients are theirs alone
+    m = M()
+    T, F, k = 33_000, 65_536, 5
+    at = np.r_[0:k, T - k:T]
+    r = np.random.default_rng(9)
+    X, W, _, _ = _whole(T, 8, 3)
+    W = [r.integers(-1, 2, s).astype(np.float64) for s in ((F, 768), (F, 768), (768, F))]
+    dY = np.zeros((T, 768))
+    dY[at] = r.integers(-1, 2, (2 * k, 768)) * (r.random((2 * k, 768)) < 0.03)
+    cfg = m.config(F, T, act="relu2", y_dtype="f32", dw_dtype="f32")
+    ws = m.Workspace(cfg)
+    Xd, Wc = _bf16(X).cuda(), [_bf16(w).cuda() for w in W]
+    y = m.fwd(cfg, ws, Xd, *Wc)
+    _same(y[at], orc.forward(X[at], *W, "relu2"), "Y")
+    g = m.bwd(cfg, ws, Xd, *Wc, torch.from_numpy(dY).float().cuda())
+    o = orc.backward(X[at], *W, dY[at], "relu2")
+    _same(g["dX"][at], o["dX"], "dX")
+    assert torch.count_nonzero(g["dX"][k:T - k]) == 0
+    for n in NAMES[1:]:
+        _same(g[n], o[n], n)
