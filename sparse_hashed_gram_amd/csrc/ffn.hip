@@ -365,17 +365,17 @@ __global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
     rows_tile<S, DX>(a, blockIdx.x, sm);
 }
 
-// v += the parts' 8 values at i, in order; four parts' loads at a time are in flight.
+// v += the parts' 8 values at i, in order; eight parts' loads at a time are in flight.
 __device__ __forceinline__ void add_parts(const float *part, int64_t size, int parts, int64_t i, float (&v)[8])
 {
-    for (int p = 0; p < parts; p += 4) {
-        float x[4][8];
+    for (int p = 0; p < parts; p += 8) {
+        float x[8][8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 8; ++q)
             if (p + q < parts)
                 load_as(part + (p + q) * size, true, i, x[q]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 8; ++q)
             if (p + q < parts) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -924,7 +924,9 @@ struct Layout {
 // launch that adds them.  turns(): a block alone on its CU is bound by latency,
 // a second one fits beside it for a third more, and from about five on the
 // CU's load path (see mfma_tile.hpp) makes them add up.  The constants are
-// measured (T = 30 ... 49,152, F = 1000 ... 4096, warm, one process):
+// measured (T = 30 ... 49,152, F = 128 ... 8000, warm, one process; over 93 pairs
+// of T and F the chosen launches take 1.00 (H and its gradients), 1.01 (Y) and 1.02
+// times (dX and the weights' gradients) the best ones' time):
 //   a step of rows: Half 0.45, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
 //   up (12 steps and epilogue): Half 4.2, Small 7.75, hidden8 22 us a block;
 //   grad (24 steps and epilogue): Half 8.6, Small 14.5, hidden8 40 us a block.
@@ -933,7 +935,7 @@ struct Layout {
 // Small), T = 49,152: Small 620, hidden8 503 us; down at T = 49,152: Small 167,
 // Mid 146 us; dW at T = 1024: Small 19.5, Square 28 us, at T = 49,152: Small
 // 532 (7 parts), Square 451 us (7 parts) against 1,132 (1 part).
-constexpr double kReduce = 3.0, kBytesPerUs = 4.5e6;
+constexpr double kReduce = 4.5, kBytesPerUs = 4.5e6;
 constexpr int kMaxRowParts = 16;   // of a [T][768] result
 
 double rounds(int64_t blocks) { return (double)((blocks + kCUs - 1) / kCUs); }
@@ -958,13 +960,18 @@ void consider(Choice &best, int shape, int parts, double us)
         best = Choice{shape, parts, us};
 }
 
-// Tiles of positions x units; 0 Half, 1 Small, 2 hidden8_kernel's.
+// Tiles of positions x units; 0 Half, 1 Small, 2 hidden8_kernel's.  A second
+// Half block on a CU costs less than the first, a chip full of Small ones more
+// than a few (gradients, T = 1800, F = 1000: Half, 464 blocks, 19 us, Small, 240, 22; T =
+// 4000, F = 264: 315 blocks 15, 160 blocks 20).
 Choice choose_hidden(int64_t T, int64_t F, bool bwd)
 {
     Choice c{};
     auto tiles = [&](int bn, int bm) { return ceil_div(T, bn) * ceil_div(F, bm / 2); };
-    consider(c, 0, 1, (bwd ? 8.6 : 4.2) * rounds(tiles(Half::BN, Half::BM)));
-    consider(c, 1, 1, (bwd ? 14.5 : 7.75) * rounds(tiles(Small::BN, Small::BM)));
+    const int64_t half = tiles(Half::BN, Half::BM), small = tiles(Small::BN, Small::BM);
+    const double h = (double)half / kCUs, m = (double)small / kCUs;
+    consider(c, 0, 1, (bwd ? 8.6 : 4.2) * (h > 1.0 && h <= 2.0 ? 1.2 + 0.4 * h : rounds(half)));
+    consider(c, 1, 1, (bwd ? 14.5 : 7.75) * (m <= 1.0 ? 1.0 + 0.3 * m : rounds(small)));
     if (T >= G8::BN && F >= G8::BM / 2)
         consider(c, 2, 1, (bwd ? 40.0 : 22.0) * rounds(tiles(G8::BN, G8::BM)));
     return c;
@@ -976,9 +983,20 @@ int64_t dw_tiles(int64_t F, int64_t Fp, int bm, int bn)
     return ceil_div(2 * Fp, bn) * (kD / bm) + (kD / bn) * ceil_div(F, bm);
 }
 
+// A step of Small tiles of the weights' gradients.  Where the operands exceed
+// the L2s, a block alone on its CU waits for them (T = 15,000, F = 400: 198 blocks
+// 0.74 us a step, 462 blocks 0.5).
+double dw_step(int64_t T, int64_t Fp, int64_t blocks)
+{
+    return T * (2 * kD + 6 * Fp) <= (32 << 20) ? 0.47 : blocks <= kCUs ? 0.74 : 0.57;
+}
+
 // A [T][768] result over `steps` stages of k; 0 Half, 1 Small, 2 Mid.  A part
 // has at least two stages, and parts only where a round of blocks holds them.
-Choice choose_rows(int64_t T, int64_t steps)
+// step: 1.4 where the weights' rows are not whole 128-byte lines, else 1; many
+// blocks feel it (Y at T = 3001: F = 2048 23 us, F = 2056 29 us), but not two Small
+// ones on a CU (T = 4000, F = 4104: 1 part 55 us, 2 parts 45).
+Choice choose_rows(int64_t T, int64_t steps, double step)
 {
     Choice c{};
     for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
@@ -986,32 +1004,47 @@ Choice choose_rows(int64_t T, int64_t steps)
         const double n = (double)ceil_div(steps, p);
         const int64_t half = ceil_div(T, Half::BN) * (kD / Half::BM) * p, small = ceil_div(T, Small::BN) * (kD / Small::BM) * p;
         if (p == 1 || half <= 2 * kCUs)
-            consider(c, 0, p, turns(half) * (0.45 * n + 2.0) + add);
+            consider(c, 0, p, turns(half) * (0.45 * (2 * half > kCUs ? step : 1.0) * n + 1.0) + add);
         if (p == 1 || small <= 2 * kCUs)
-            consider(c, 1, p, turns(small) * (0.62 * n + 2.0) + add);
+            consider(c, 1, p, turns(small) * (0.62 * (2 * small > kCUs && small <= kCUs ? step : 1.0) * n + 2.0) + add);
         if (p == 1)
             consider(c, 2, p, turns(ceil_div(T, Mid::BN) * (kD / Mid::BM)) * (0.80 * n + 2.0));
     }
     return c;
 }
 
-// dX and the weights' gradients in one launch, dX on Half or Small tiles:
-// blocks of two lengths, so their mean counts where there are more than CUs.
+// dX and the weights' gradients in one launch, dX on Half or Small tiles: two
+// blocks fit on a CU, and dX's are dispatched first.  While not all are resident
+// the CUs' work adds up; what is left then is a launch of its own, in which a
+// block that shares its CU takes about half as long again (T = 4096, F = 2048,
+// 480 blocks: 67 us expected, 70 measured; 6,000 x 2048, 570: 137 / 131; 6,000 x
+// 4104, 870: 198 / 199; 2,500 x 1000, 264: 32 / 35).
 Choice choose_tail(int64_t T, int64_t F, int64_t Fp)
 {
     Choice c{};
-    const int64_t steps = 2 * Fp / kBK;
-    const double dn = (double)dw_tiles(F, Fp, Small::BM, Small::BN), dt = 0.47 * ceil_div(T, kBK) + 1.3;
-    auto one = [&](int shape, int p, int64_t n, double t) {
-        const int64_t all = n * p + (int64_t)dn;
-        const double longest = t > dt ? t : dt, mean = (n * p * t + dn * dt) / all, r = rounds(all);
-        const double us = r <= 1.0 ? 1.2 * longest : (1.1 * r * mean > longest ? 1.1 * r * mean : longest);
-        if (p == 1 || n * p <= 2 * (int64_t)kCUs)
-            consider(c, shape, p, us + (p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0));
+    const int64_t steps = 2 * Fp / kBK, dn = grid_blocks((uint32_t)dw_tiles(F, Fp, Small::BM, Small::BN)), slots = 2 * kCUs;
+    const double dt = 0.47 * ceil_div(T, kBK) + 1.3;
+    auto one = [&](int shape, int p, int64_t tiles, double t) {
+        const int64_t n = grid_blocks((uint32_t)(tiles * p));   // slots are an XCD's: whole eighths
+        if (p > 1 && n > slots)
+            return;
+        const double add = p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0;
+        double us = 0.0;
+        int64_t x = n, w = dn;   // blocks left
+        while (x + w > slots) {
+            const int64_t xs = x < slots ? x : slots, ws = slots - xs;
+            us += (xs * t + ws * dt) / kCUs;
+            x -= xs;
+            w -= ws;
+        }
+        const double last = x && t > dt ? t : dt, sum = (x * t + w * dt) / kCUs;
+        const double alone = (x + w <= kCUs ? 1.1 : 1.45) * last, longest = (n + dn <= kCUs ? 1.1 : 1.45) * t;
+        us += sum > alone ? sum : alone;
+        consider(c, shape, p, add + (us > longest ? us : longest));
     };
     for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
         const double n = (double)ceil_div(steps, p);
-        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.45 * n + 2.0);
+        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.45 * n + 1.0);
         one(1, p, ceil_div(T, Small::BN) * (kD / Small::BM), 0.62 * n + 2.0);
     }
     return c;
@@ -1031,8 +1064,9 @@ Choice choose_dw(int64_t T, int64_t F, int64_t Fp)
     Choice c{};
     const int64_t steps = ceil_div(T, kBK);
     for (int p = 1; p <= kMaxParts && p <= steps; ++p) {
-        const double add = p > 1 ? kReduce + p * Fp * (2.0 * 4 * 3 * kD) / kBytesPerUs : 0.0, n = (double)ceil_div(steps, p);
-        consider(c, 0, p, rounds(p * dw_tiles(F, Fp, Small::BM, Small::BN)) * (0.47 * n + 1.3) + add);
+        const double add = p > 1 ? 3.0 + p * Fp * (2.0 * 4 * 3 * kD) / kBytesPerUs : 0.0, n = (double)ceil_div(steps, p);
+        const int64_t small = p * dw_tiles(F, Fp, Small::BM, Small::BN);
+        consider(c, 0, p, rounds(small) * (dw_step(T, Fp, small) * n + 1.3) + add);
         consider(c, 1, p, rounds(p * dw_tiles(F, Fp, Square::BM, Square::BN)) * (1.47 * n + 3.5) + add);
     }
     return c;
@@ -1207,14 +1241,14 @@ void grad(const Args &a, int act, hipStream_t s)
 template <bool DX>
 void rows(const Args &a, hipStream_t s)
 {
-    const Choice c = choose_rows(a.T, (DX ? 2 : 1) * a.Fp / kBK);
+    const Choice c = choose_rows(a.T, (DX ? 2 : 1) * a.Fp / kBK, !DX && a.F % kBK ? 1.4 : 1.0);
     (c.shape == 0 ? launch_rows<Half, DX> : c.shape == 1 ? launch_rows<Small, DX> : launch_rows<Mid, DX>)(a, c.parts, s);
 }
 
 // dX and the weights' gradients
 void tail(const Args &a, const DwArgs &d, hipStream_t s)
 {
-    const Choice both = choose_tail(a.T, a.F, a.Fp), x = choose_rows(a.T, 2 * a.Fp / kBK), w = choose_dw(a.T, a.F, a.Fp);
+    const Choice both = choose_tail(a.T, a.F, a.Fp), x = choose_rows(a.T, 2 * a.Fp / kBK, 1.0), w = choose_dw(a.T, a.F, a.Fp);
     if (both.us < x.us + w.us + 2.5) {
         (both.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, both.parts, d, s);
         return;
