@@ -283,16 +283,19 @@ def embed_fwd_drop(cfg: NgramConfig, W_b: torch.Tensor, W_t: torch.Tensor | None
     T = tokens.numel()
     dev = tokens.device
     _check_tables(cfg, W_b, W_t)
-    if out is None:
-        out = torch.empty((T, DIM), dtype=cfg.out_torch_dtype, device=dev)
     pw = None if W_t is None else _marshal.ptr(W_t, "W_t", dev, cfg.torch_dtype)
-    po = _marshal.ptr(out, "out", dev, cfg.out_torch_dtype, (T, DIM))
+    pt = _marshal.ptr(tokens, "tokens", dev, torch.int32)
+    if out is None:   # (1 us less than torch.empty)
+        out = torch.empty_strided((T, DIM), (DIM, 1), dtype=cfg.out_torch_dtype, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _marshal.ptr(out, "out", dev, cfg.out_torch_dtype, (T, DIM))
     if ws is not None and ws.tensor.device != dev:
         raise ValueError(f"the workspace is on {ws.tensor.device}, the tokens on {dev}")
     _check_rng(spec, dev)
     _check("ngram_embed_fwd_drop", _marshal.enqueue(
-        lib().ngram_embed_fwd_drop, dev, cfg, _marshal.ptr(W_b, "W_b", dev, cfg.torch_dtype), pw,
-        _marshal.ptr(tokens, "tokens", dev, torch.int32), T, spec, po, _ws(ws)))
+        lib().ngram_embed_fwd_drop, dev, cfg, _marshal.ptr(W_b, "W_b", dev, cfg.torch_dtype), pw, pt, T, spec, po,
+        _ws(ws)))
     return out
 
 
