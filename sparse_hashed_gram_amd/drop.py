@@ -109,8 +109,10 @@ def spec(p: float, seed: int = 0, offset: int = 0, rng: torch.Tensor | None = No
 
 
 def _check_rng(s: DropSpec, device: torch.device):
-    if s.rng and s.rng_tensor.device != device:
-        raise ValueError(f"rng is on {s.rng_tensor.device}, the call's other tensors on {device}")
+    if s.rng:
+        t = getattr(s, "rng_tensor", None)   # None: a DropSpec filled in by hand
+        if t is not None and t.device != device:
+            raise ValueError(f"rng is on {t.device}, the call's other tensors on {device}")
 
 
 def _dtype(t, name: str) -> int:

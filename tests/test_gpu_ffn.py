@@ -308,6 +308,27 @@ def test_bitwise_repeatable_and_on_another_stream(T, F):
     assert all(torch.equal(g[k], g2[k]) for k in NAMES)
 
 
+def test_two_streams_at_once():
+    # calls of different sizes and masks in flight together, each with its workspace
+    m, d = M(), D()
+    jobs = []
+    for i, (T, F) in enumerate(((1500, 1032), (70, 2048), (4100, 256), (9, 520))):
+        X, W, dY, _ = _real(T, F, 30 + i)
+        cfg = m.config(F, T)
+        jobs.append((cfg, m.Workspace(cfg), _bf16(X).cuda(), [_bf16(w).cuda() for w in W], _bf16(dY).cuda(),
+                     d.spec(0.3, i, 5), torch.cuda.Stream()))
+    want = [(m.fwd(c, ws, X, *W, drop=s), m.bwd(c, ws, X, *W, dY, drop=s)) for c, ws, X, W, dY, s, _ in jobs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for c, ws, X, W, dY, s, st in jobs:
+            with torch.cuda.stream(st):
+                got.append((m.fwd(c, ws, X, *W, drop=s), m.bwd(c, ws, X, *W, dY, drop=s)))
+        torch.cuda.synchronize()
+        for (y, g), (y0, g0) in zip(got, want):
+            assert torch.equal(y, y0) and all(torch.equal(g[k], g0[k]) for k in NAMES)
+
+
 def test_graph_replays():
     m, d = M(), D()
     T, F = 333, 520
