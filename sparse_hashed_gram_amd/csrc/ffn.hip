@@ -927,7 +927,7 @@ struct Layout {
 // measured (T = 30 ... 49,152, F = 128 ... 8000, warm, one process; over 93 pairs
 // of T and F the chosen launches take 1.00 (H and its gradients), 1.01 (Y) and 1.02
 // times (dX and the weights' gradients) the best ones' time):
-//   a step of rows: Half 0.45, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
+//   a step of rows: Half 0.45 - 0.5, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
 //   up (12 steps and epilogue): Half 4.2, Small 7.75, hidden8 22 us a block;
 //   grad (24 steps and epilogue): Half 8.6, Small 14.5, hidden8 40 us a block.
 // E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 24 us (Half / Small / hidden8), T =
@@ -935,7 +935,7 @@ struct Layout {
 // Small), T = 49,152: Small 620, hidden8 503 us; down at T = 49,152: Small 167,
 // Mid 146 us; dW at T = 1024: Small 19.5, Square 28 us, at T = 49,152: Small
 // 532 (7 parts), Square 451 us (7 parts) against 1,132 (1 part).
-constexpr double kReduce = 4.5, kBytesPerUs = 4.5e6;
+constexpr double kBytesPerUs = 4.5e6;
 constexpr int kMaxRowParts = 16;   // of a [T][768] result
 
 double rounds(int64_t blocks) { return (double)((blocks + kCUs - 1) / kCUs); }
@@ -948,6 +948,9 @@ double turns(int64_t blocks)
     const int64_t r = (blocks + kCUs - 1) / kCUs;
     return r < 5 ? few[r] : 0.93 * (double)r;
 }
+
+// the parts of a [T][768] result, written, read and added in a launch of their own
+double reduce_us(int64_t T, int p) { return 3.0 + 0.1 * p + p * T * (2.0 * 4 * kD) / kBytesPerUs; }
 
 struct Choice {
     int shape, parts;   // index into the candidates
@@ -1000,11 +1003,11 @@ Choice choose_rows(int64_t T, int64_t steps, double step)
 {
     Choice c{};
     for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
-        const double add = p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0;
+        const double add = p > 1 ? reduce_us(T, p) : 0.0;
         const double n = (double)ceil_div(steps, p);
         const int64_t half = ceil_div(T, Half::BN) * (kD / Half::BM) * p, small = ceil_div(T, Small::BN) * (kD / Small::BM) * p;
         if (p == 1 || half <= 2 * kCUs)
-            consider(c, 0, p, turns(half) * (0.45 * (2 * half > kCUs ? step : 1.0) * n + 1.0) + add);
+            consider(c, 0, p, turns(half) * ((2 * half > kCUs ? 0.45 * step : 0.5) * n + 1.0) + add);
         if (p == 1 || small <= 2 * kCUs)
             consider(c, 1, p, turns(small) * (0.62 * (2 * small > kCUs && small <= kCUs ? step : 1.0) * n + 2.0) + add);
         if (p == 1)
@@ -1028,7 +1031,7 @@ Choice choose_tail(int64_t T, int64_t F, int64_t Fp)
         const int64_t n = grid_blocks((uint32_t)(tiles * p));   // slots are an XCD's: whole eighths
         if (p > 1 && n > slots)
             return;
-        const double add = p > 1 ? kReduce + p * T * (2.0 * 4 * kD) / kBytesPerUs : 0.0;
+        const double add = p > 1 ? reduce_us(T, p) : 0.0;
         double us = 0.0;
         int64_t x = n, w = dn;   // blocks left
         while (x + w > slots) {
@@ -1044,7 +1047,7 @@ Choice choose_tail(int64_t T, int64_t F, int64_t Fp)
     };
     for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
         const double n = (double)ceil_div(steps, p);
-        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.45 * n + 1.0);
+        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.5 * n + 1.0);
         one(1, p, ceil_div(T, Small::BN) * (kD / Small::BM), 0.62 * n + 2.0);
     }
     return c;
