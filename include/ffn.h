@@ -17,7 +17,9 @@
  * Precision: products of bf16 values on the matrix cores, summed in fp32;
  * the activation and its derivative in fp32 from the fp32 sums.  Rounded to
  * bf16 (nearest, ties to even) on the way, each once and only because it is an
- * operand of a further product: H, dG and dU, and dY where it is fp32.  The
+ * operand of a further product: H, dG and dU, and dY where it is fp32.  (Calls
+ * of at most 32 positions and T F <= 8192 keep 16 bits of H, dG and dU, as two bf16
+ * values: so few roundings need not average out.)  The
  * scale of the dropout is applied to fp32 sums.  Y, dX and the weights'
  * gradients are rounded once, at the end.  The backward computes G and U
  * again from X: the forward keeps nothing, which saves 4 T F bytes of

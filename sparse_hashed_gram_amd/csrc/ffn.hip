@@ -138,6 +138,21 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8])
                       bf16_pack_rne(v[6], v[7]));
 }
 
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]);
+
+// What rounding v to bf16 (r) left, itself in bf16: together 16 bits of it.
+__device__ __forceinline__ float left_over(float v, float r) { return isinf(r) ? 0.0f : v - r; }
+
+__device__ __forceinline__ uint4 pack8_left(const float (&v)[8], const uint4 &rounded)
+{
+    float r[8];
+    unpack8(rounded, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        r[e] = left_over(v[e], r[e]);
+    return pack8(r);
+}
+
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8])
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -238,6 +253,7 @@ struct Args {
     int32_t out_f32;
     int32_t parts;           // parts of k of a [T][768] result
     float *part;             // [parts][T][768] where parts > 1
+    uint16_t *lo;            // of wide_rows: what S's rounding left, laid out as S; else NULL
     drop::Mask mask;
 };
 
@@ -331,8 +347,12 @@ __device__ __forceinline__ void rows_tile(const Args &a, uint32_t block, uint8_t
     clear(acc);
     if constexpr (DX) {
         const Operand A{{a.Wg, a.Wu}, kD, d0, kD, (int32_t)a.Fp, (int32_t)a.F, 0};
-        const Operand B{{a.S, a.S}, 3 * a.Fp, n0, a.T, (int32_t)a.Fp, (int32_t)a.F, 0};
-        S::template run<true, false, S::WM>(A, B, k0, k1 - k0, sm, acc);
+        for (const uint16_t *from = a.S;; from = a.lo) {
+            const Operand B{{from, from}, 3 * a.Fp, n0, a.T, (int32_t)a.Fp, (int32_t)a.F, 0};
+            S::template run<true, false, S::WM>(A, B, k0, k1 - k0, sm, acc);
+            if (!a.lo || from == a.lo)
+                break;
+        }
     } else {
         S::template run<false, false, S::WM>(rows_of(a.Wd, a.F, d0, kD, a.F), rows_of(a.S, a.Fp, n0, a.T, a.F), k0,
                                              k1 - k0, sm, acc);
@@ -424,8 +444,13 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
         auto put = [&](int which) {
             return [&, which](int n, int m, const float (&v)[8]) {
                 const int64_t t = tw + n, f = fw + m;
-                if (t < a.T && f < a.F)
-                    *reinterpret_cast<uint4 *>(a.S + t * 3 * a.Fp + which * a.Fp + f) = pack8(v);
+                if (t < a.T && f < a.F) {
+                    const int64_t i = t * 3 * a.Fp + which * a.Fp + f;
+                    const uint4 r = pack8(v);
+                    *reinterpret_cast<uint4 *>(a.S + i) = r;
+                    if (a.lo)
+                        *reinterpret_cast<uint4 *>(a.lo + i) = pack8_left(v, r);
+                }
             };
         };
         // H, then dU over the gate sums' place, dG over the up sums'
@@ -637,16 +662,27 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-constexpr int kFewWaves = 4;
+constexpr int kFewT = 32, kFewWaves = 4;
 constexpr int kFewDown = 8;   // wavefronts of a down block
 
 bool few_rows(int64_t T, int64_t F)
 {
-    return T <= 32 && F <= 8192 && T * F <= 96 * 1024;
+    return T <= kFewT && F <= 8192 && T * F <= 96 * 1024;
+}
+
+// Calls of few values also keep 16 bits of H, dG and dU, as two bf16 values (the
+// rounded one and what that left): with few values behind an output, a rounding
+// that makes its error 1.4 times that of its own rounding alone makes it up to 1.9
+// times in some calls.  Kernels of the forward at 1 x 2048 7.8 -> 9 us (a call is the
+// host's 10.7), of the backward at 1 x 424 19 -> 20; for more values the roundings
+// average out and the products would double.
+bool wide_rows(int64_t T, int64_t F)
+{
+    return T <= kFewT && T * F <= 8192;
 }
 
 // H of 16 hidden units, NT tiles of 16 positions; a wavefront takes a quarter of k.
-template <int ACT, int NT>
+template <int ACT, int NT, bool WIDE>
 __global__ __launch_bounds__(64 * kFewWaves) void up_few_kernel(Args a)
 {
     constexpr int STEPS = kD / (32 * kFewWaves);   // 6
@@ -697,15 +733,20 @@ __global__ __launch_bounds__(64 * kFewWaves) void up_few_kernel(Args a)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             h[e] = act<ACT, false>(sg[e], d) * su[e];
-        uint2 o;
+        uint2 o, l;
         o.x = ngram::bf16_pack_rne(h[0], h[1]);
         o.y = ngram::bf16_pack_rne(h[2], h[3]);
         *reinterpret_cast<uint2 *>(a.S + t * a.Fp + ff) = o;
+        if constexpr (WIDE) {
+            l.x = ngram::bf16_pack_rne(left_over(h[0], ngram::bf16_lo(o.x)), left_over(h[1], ngram::bf16_hi(o.x)));
+            l.y = ngram::bf16_pack_rne(left_over(h[2], ngram::bf16_lo(o.y)), left_over(h[3], ngram::bf16_hi(o.y)));
+            *reinterpret_cast<uint2 *>(a.lo + t * a.Fp + ff) = l;
+        }
     }
 }
 
 // Y of 16 outputs; a wavefront takes every eighth step of 32 values of k.
-template <int NT>
+template <int NT, bool WIDE>
 __global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
 {
     constexpr int U = 4;   // steps in flight
@@ -713,28 +754,34 @@ __global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15;
     const int64_t d0 = (int64_t)blockIdx.x * 16;
     const uint16_t *pw = a.Wd + (d0 + r) * a.F;
-    const uint16_t *ph[NT];
+    int64_t ph[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        ph[n] = a.S + (16 * n + r < a.T ? 16 * n + r : a.T - 1) * a.Fp;
+        ph[n] = (16 * n + r < a.T ? 16 * n + r : a.T - 1) * a.Fp;
     f32x4 acc[NT] = {};
     const bf16x8 zero = {};
     for (int64_t k0 = (int64_t)w * 32 + 8 * (lane >> 4); k0 - 8 * (lane >> 4) < a.F; k0 += U * kFewDown * 32) {
-        bf16x8 x[U], h[U][NT];
+        bf16x8 x[U], h[U][NT], l[U][NT];
 #pragma unroll
         for (int s = 0; s < U; ++s) {
             const int64_t k = k0 + s * (kFewDown * 32);
             const bool in = k < a.F;
             x[s] = in ? *reinterpret_cast<const bf16x8 *>(pw + k) : zero;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                h[s][n] = in ? *reinterpret_cast<const bf16x8 *>(ph[n] + k) : zero;
+            for (int n = 0; n < NT; ++n) {
+                h[s][n] = in ? *reinterpret_cast<const bf16x8 *>(a.S + ph[n] + k) : zero;
+                if constexpr (WIDE)
+                    l[s][n] = in ? *reinterpret_cast<const bf16x8 *>(a.lo + ph[n] + k) : zero;
+            }
         }
 #pragma unroll
         for (int s = 0; s < U; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
                 acc[n] = mfma16(x[s], h[s][n], acc[n]);
+                if constexpr (WIDE)
+                    acc[n] = mfma16(x[s], l[s][n], acc[n]);
+            }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -757,7 +804,7 @@ __global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
 }
 
 struct DwArgs {
-    const uint16_t *X, *dY, *S;
+    const uint16_t *X, *dY, *S, *lo;   // lo: as in Args
     int64_t T, F, Fp;
     uint32_t tiles_f2, tiles_d;     // dWg and dWu: tiles of 2 Fp rows x 768
     uint32_t tiles_e, tiles_h;      // dWd: tiles of 768 rows x F
@@ -817,13 +864,19 @@ __device__ __forceinline__ void dw_tile(const DwArgs &a, uint32_t block, uint8_t
     }
     const int64_t nk = (a.T + kBK - 1) / kBK, k0 = part * nk / a.parts * kBK, k1 = (part + 1) * nk / a.parts * kBK;
     const int64_t ls = 3 * a.Fp, valid = (a.T < k1 ? a.T : k1) - k0;
-    const Operand A = down ? rows_of(a.S + 2 * a.Fp + k0 * ls, ls, m0, a.F, valid)
-                           : rows_of(a.X + k0 * kD, kD, m0, kD, valid);
-    const Operand B = down ? rows_of(a.dY + k0 * kD, kD, n0, kD, valid)
-                           : rows_of(a.S + k0 * ls, ls, n0, 2 * a.Fp, valid);
+    Operand A = down ? rows_of(a.S + 2 * a.Fp + k0 * ls, ls, m0, a.F, valid)
+                     : rows_of(a.X + k0 * kD, kD, m0, kD, valid);
+    Operand B = down ? rows_of(a.dY + k0 * kD, kD, n0, kD, valid)
+                     : rows_of(a.S + k0 * ls, ls, n0, 2 * a.Fp, valid);
+    int64_t K = k1 - k0;
+    if (a.lo) {   // one stage of positions: the same again with the left-overs
+        A.seg = B.seg = kBK;
+        (down ? A : B).src[1] = a.lo + (down ? 2 * a.Fp : 0);
+        K = 2 * kBK;
+    }
     f32x16 acc[S::WM][S::WN];
     clear(acc);
-    S::template run<true, true, S::WM>(A, B, 0, k1 - k0, sm, acc);
+    S::template run<true, true, S::WM>(A, B, 0, K, sm, acc);
     const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
     float *lds = reinterpret_cast<float *>(sm + w * Rows<S::WM>::BYTES);
     float *pp = a.parts > 1 ? a.part + part * (3 * a.Fp * kD) : nullptr;
@@ -1175,13 +1228,13 @@ void launch_rows(Args a, int parts, hipStream_t s)
     reduce_rows<DX>(a, s);
 }
 
-template <int NT>
+template <int NT, bool WIDE>
 void launch_few(const Args &a, int act, hipStream_t s)
 {
-    auto k = act == FFN_ACT_SILU ? up_few_kernel<FFN_ACT_SILU, NT>
-             : act == FFN_ACT_GELU ? up_few_kernel<FFN_ACT_GELU, NT> : up_few_kernel<FFN_ACT_RELU2, NT>;
+    auto k = act == FFN_ACT_SILU ? up_few_kernel<FFN_ACT_SILU, NT, WIDE>
+             : act == FFN_ACT_GELU ? up_few_kernel<FFN_ACT_GELU, NT, WIDE> : up_few_kernel<FFN_ACT_RELU2, NT, WIDE>;
     k<<<blocks(a.F, 16), 64 * kFewWaves, 0, s>>>(a);
-    down_few_kernel<NT><<<kD / 16, 64 * kFewDown, 0, s>>>(a);
+    down_few_kernel<NT, WIDE><<<kD / 16, 64 * kFewDown, 0, s>>>(a);
 }
 
 template <class S>
@@ -1252,7 +1305,7 @@ void rows(const Args &a, hipStream_t s)
 void tail(const Args &a, const DwArgs &d, hipStream_t s)
 {
     const Choice both = choose_tail(a.T, a.F, a.Fp), x = choose_rows(a.T, 2 * a.Fp / kBK, 1.0), w = choose_dw(a.T, a.F, a.Fp);
-    if (both.us < x.us + w.us + 2.5) {
+    if (a.lo || both.us < x.us + w.us + 2.5) {
         (both.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, both.parts, d, s);
         return;
     }
@@ -1378,13 +1431,15 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.out = Y;
     a.out_f32 = cfg->y_dtype == FFN_DTYPE_F32;
     hipStream_t s = (hipStream_t)stream;
+    if (wide_rows(T, a.F))
+        a.lo = (uint16_t *)a.part;   // 2 T Fp <= 16,384 T bytes; part holds 49,152 T
     if (!few_rows(T, a.F)) {
         up(a, cfg->act, s);
         rows<false>(a, s);
-    } else if (T > 16) {
-        launch_few<2>(a, cfg->act, s);
+    } else if (a.lo) {
+        (T > 16 ? launch_few<2, true> : launch_few<1, true>)(a, cfg->act, s);
     } else {
-        launch_few<1>(a, cfg->act, s);
+        (T > 16 ? launch_few<2, false> : launch_few<1, false>)(a, cfg->act, s);
     }
     return done();
 }
@@ -1445,6 +1500,12 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     d.S = a.S;
     d.scale = a.mask.scale;
     d.part = (float *)((uint8_t *)ws + L.part);
+    if (wide_rows(T, a.F)) {
+        // behind the parts of dX; the whole is at least 73,728 Fp bytes
+        static_assert(kMaxRowParts * kFewT * kD * 4 + 6 * kFewT * 64 <= 4 * kMaxParts * 3 * kD * 64, "room at Fp = 64");
+        a.lo = (uint16_t *)(a.part + kMaxRowParts * kFewT * kD);
+        d.lo = a.lo;
+    }
     grad(a, cfg->act, s);
     tail(a, d, s);
     return done();

@@ -221,6 +221,40 @@ def test_real_values(T, F, p, yt, wt, kind):
         _hold(g[k], *o[k], g[k].dtype == torch.bfloat16, k)
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu", "relu2"])
+@pytest.mark.parametrize("T,F", [(1, 128), (1, 2048), (1, 8192), (2, 424), (3, 2056), (7, 136), (16, 512), (17, 480), (32, 256), (31, 128)])
+def test_few_positions_round_once(T, F, kind):
+    # H, dG and dU keep 16 bits here, so a result's own rounding, of 2^-8 / sqrt(3) of the
+    # value at most on average, is what is left: with it the operands' 2^-17 and
+    # the fp32 sums (2^-24 times a few hundred).  A root of n values' squares strays
+    # from its expectation by about 1 / sqrt(n) of it, n at least 768 here, and a
+    # rounding's is well below its most: for mantissas spread evenly 0.7 of it.
+    m, d = M(), D()
+    X, W, dY, _ = _real(T, F, 50)
+    cfg = m.config(F, T, act=kind)
+    ws, spec = m.Workspace(cfg), d.spec(0.2, 3, 4)
+    factor = orcd.keep(T, 768, 0.2, 3, 4) * (65536 / (65536 - orcd.threshold(0.2)))
+    Xd, Wc = _bf16(X).cuda(), [_bf16(w).cuda() for w in W]
+    got = {"Y": m.fwd(cfg, ws, Xd, *Wc, drop=spec), **m.bwd(cfg, ws, Xd, *Wc, _bf16(dY).cuda(), drop=spec)}
+    want = {"Y": orc.forward(X, *W, kind, factor), **orc.backward(X, *W, dY, kind, factor)}
+    for k, v in want.items():
+        assert np.linalg.norm(_f64(got[k]) - v) <= (B / np.sqrt(3) + 2.0 ** -12) * np.linalg.norm(v), k
+
+
+def test_few_positions_past_the_largest_bf16():
+    # G = 2^43, U = 2^42 (1 - 2^-10): H = 2^128 (1 - 2^-10) is finite in fp32 and
+    # rounds to infinity in bf16; what that leaves is taken as 0, not as -infinity
+    m = M()
+    F = 64
+    X, Wg, Wu = (np.zeros((n, 768)) for n in (2, F, F))
+    X[:, 0], X[:, 1] = 2.0 ** 43, 2.0 ** 33
+    Wg[:, 0] = 1.0
+    Wu[:, 0], Wu[:, 1] = 0.498046875, 1.5
+    cfg = m.config(F, 2, act="relu2", y_dtype="f32")
+    y = m.fwd(cfg, m.Workspace(cfg), *(_bf16(a).cuda() for a in (X, Wg, Wu, np.ones((768, F)))))
+    assert torch.all(torch.isinf(y) & (y > 0))
+
+
 def test_gradients_against_differences_of_the_forward():
     # along a random direction, with fp32 results: the forward's own rounding of H
     # (2^-8 of it) is the noise, so the step is large and the check coarse
