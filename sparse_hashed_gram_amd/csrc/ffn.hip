@@ -417,13 +417,18 @@ __global__ __launch_bounds__(256) void rows_reduce_kernel(Args a)
 }
 
 // dG, dU and H of BN positions x BM / 2 hidden units: the gate and up sums
-// again as in up_kernel, then dH of the same tile.
+// again as in up_kernel, and dH of the same tile.  Half tiles take both
+// products' steps together (257 x 1000: 11.0 -> 9.9 us, the whole backward 29.2 ->
+// 26.1); the larger ones, bound by more than a step's chain, one after the other,
+// in the LDS of one.
 template <class S, int ACT>
 __global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
 {
     constexpr int HB = S::WM / 2;
+    constexpr bool TOGETHER = S::WN == 1;
+    using P = Pair<false, true, false, S::WM, HB, S::WN, S::GM, S::GN>;
     __shared__ __align__(16) uint8_t sm[smem_for<S, HB>(
-        cmax(S::template smem<false, false, S::WM>(), S::template smem<true, false, HB>()))];
+        TOGETHER ? P::SMEM : cmax(S::template smem<false, false, S::WM>(), S::template smem<true, false, HB>()))];
     uint32_t tt, ot;
     if (!tile_of(blockIdx.x, a.tiles_t, a.tiles_o, tt, ot))
         return;
@@ -431,10 +436,15 @@ __global__ __launch_bounds__(S::THREADS) void grad_kernel(Args a)
     f32x16 acc[S::WM][S::WN], dh[HB][S::WN];
     clear(acc);
     const Operand A{{a.Wg, a.Wu}, kD, f0, a.F, INT32_MAX, kD, 32 * HB};
-    S::template run<false, false, S::WM>(A, rows_of(a.X, kD, n0, a.T, kD), 0, kD, sm, acc);
-    clear(dh);
-    S::template run<true, false, HB>(rows_of(a.Wd, a.F, f0, a.F, kD),
-                                                 rows_of(a.dY, kD, n0, a.T, kD), 0, kD, sm, dh);
+    const Operand X = rows_of(a.X, kD, n0, a.T, kD), Wd = rows_of(a.Wd, a.F, f0, a.F, kD), dY = rows_of(a.dY, kD, n0, a.T, kD);
+    if constexpr (TOGETHER) {
+        clear(dh);
+        P::run(A, X, Wd, dY, kD, sm, acc, dh);
+    } else {
+        S::template run<false, false, S::WM>(A, X, 0, kD, sm, acc);
+        clear(dh);
+        S::template run<true, false, HB>(Wd, dY, 0, kD, sm, dh);
+    }
     const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
     float *lds = reinterpret_cast<float *>(sm + w * Rows<HB>::BYTES);
     const int64_t fw = f0 + wm * 32 * HB;
@@ -982,7 +992,7 @@ struct Layout {
 // times (dX and the weights' gradients) the best ones' time):
 //   a step of rows: Half 0.45 - 0.5, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
 //   up (12 steps and epilogue): Half 4.2, Small 7.75, hidden8 22 us a block;
-//   grad (24 steps and epilogue): Half 8.6, Small 14.5, hidden8 40 us a block.
+//   grad (24 steps and epilogue): Half 7.6 (8.6 past two a CU), Small 14.5, hidden8 40 us a block.
 // E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 24 us (Half / Small / hidden8), T =
 // 49,152: Small 371, hidden8 263 us; grad at T = 100: 11.4 / 15.3 us (Half /
 // Small), T = 49,152: Small 620, hidden8 503 us; down at T = 49,152: Small 167,
@@ -1026,7 +1036,7 @@ Choice choose_hidden(int64_t T, int64_t F, bool bwd)
     auto tiles = [&](int bn, int bm) { return ceil_div(T, bn) * ceil_div(F, bm / 2); };
     const int64_t half = tiles(Half::BN, Half::BM), small = tiles(Small::BN, Small::BM);
     const double h = (double)half / kCUs, m = (double)small / kCUs;
-    consider(c, 0, 1, (bwd ? 8.6 : 4.2) * (h > 1.0 && h <= 2.0 ? 1.2 + 0.4 * h : rounds(half)));
+    consider(c, 0, 1, h <= 2.0 ? (bwd ? 7.6 : 4.2) * (h > 1.0 ? 1.2 + 0.4 * h : 1.0) : (bwd ? 8.6 : 4.2) * rounds(half));
     consider(c, 1, 1, (bwd ? 14.5 : 7.75) * (m <= 1.0 ? 1.0 + 0.3 * m : rounds(small)));
     if (T >= G8::BN && F >= G8::BM / 2)
         consider(c, 2, 1, (bwd ? 40.0 : 22.0) * rounds(tiles(G8::BN, G8::BM)));

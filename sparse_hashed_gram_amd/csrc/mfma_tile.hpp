@@ -481,6 +481,79 @@ __device__ __forceinline__ void product(const Operand &A, const Operand &B, int3
     __syncthreads();
 }
 
+// Two products over the same K, step by step together.  A step of a small tile is
+// its own chain of LDS reads, dependent matrix instructions and a barrier (0.3
+// us for two instructions a sub-step), so two of them cost little more than one.
+template <typename T1, typename T2, bool AK1, bool AK2, bool BK, int M1, int M2, int WN>
+__device__ __forceinline__ void pair_steps(T1 &t1, T2 &t2, int kt, int nk, lds_u8 *__restrict__ s0,
+                                           lds_u8 *__restrict__ s1, lds_u8 *__restrict__ u0,
+                                           lds_u8 *__restrict__ u1, bf16x8 (&a1)[2][M1], bf16x8 (&b1)[2][WN],
+                                           bf16x8 (&a2)[2][M2], bf16x8 (&b2)[2][WN], f32x16 (&acc1)[M1][WN],
+                                           f32x16 (&acc2)[M2][WN])
+{
+    auto sub = [&](const lds_u8 *s, const lds_u8 *u, int kk, int from) {
+        sub_step<T1, AK1, BK>(t1, s, kk, a1[from], b1[from], a1[1 - from], b1[1 - from], acc1);
+        sub_step<T2, AK2, BK>(t2, u, kk, a2[from], b2[from], a2[1 - from], b2[1 - from], acc2);
+    };
+    sub(s0, u0, 1, 0);
+    sub(s0, u0, 2, 1);
+    sub(s0, u0, 3, 0);
+    wait_vmcnt<0>();
+    barrier_nofence();
+    sub(s1, u1, 0, 1);
+    if (kt + 1 >= nk)
+        return;
+    if (kt + 2 < nk) {
+        t1.issue(s0);
+        t2.issue(u0);
+    }
+    sub(s1, u1, 1, 0);
+    sub(s1, u1, 2, 1);
+    sub(s1, u1, 3, 0);
+    wait_vmcnt<0>();
+    barrier_nofence();
+    sub(s0, u0, 0, 1);
+    if (kt + 3 < nk) {
+        t1.issue(s1);
+        t2.issue(u1);
+    }
+}
+
+// acc1 += A1 B1, acc2 += A2 B2 over K values of k (at least two stages).
+template <bool AK1, bool AK2, bool BK, int M1, int M2, int WN, int GM, int GN>
+struct Pair {
+    using T1 = Tile<AK1, BK, M1, WN, GM, GN>;
+    using T2 = Tile<AK2, BK, M2, WN, GM, GN>;
+    static constexpr uint32_t SMEM = T1::SMEM + T2::SMEM;
+
+    static __device__ __forceinline__ void run(const Operand &A1, const Operand &B1, const Operand &A2,
+                                               const Operand &B2, int32_t K, uint8_t *sm, f32x16 (&acc1)[M1][WN],
+                                               f32x16 (&acc2)[M2][WN])
+    {
+        static_assert(GM * GN <= 4, "the four-wavefront loop");
+        T1 t1;
+        T2 t2;
+        lds_u8 *s0, *s1, *u0, *u1;
+        places(sm, T1::STAGE, s0, s1);
+        places(sm + T1::SMEM, T2::STAGE, u0, u1);
+        const int nk = K / kBK;
+        t1.init(A1, B1, 0);
+        t2.init(A2, B2, 0);
+        t1.issue(s0);
+        t2.issue(u0);
+        t1.issue(s1);
+        t2.issue(u1);
+        wait_vmcnt<T1::LA::L + T1::LB::L + T2::LA::L + T2::LB::L>();
+        barrier_nofence();
+        bf16x8 a1[2][M1], b1[2][WN], a2[2][M2], b2[2][WN];
+        t1.read(s0, 0, a1[0], b1[0]);
+        t2.read(u0, 0, a2[0], b2[0]);
+        for (int kt = 0; kt < nk; kt += 2)
+            pair_steps<T1, T2, AK1, AK2, BK>(t1, t2, kt, nk, s0, s1, u0, u1, a1, b1, a2, b2, acc1, acc2);
+        __syncthreads();
+    }
+};
+
 template <int WM, int WN>
 __device__ __forceinline__ void clear(f32x16 (&acc)[WM][WN])
 {
