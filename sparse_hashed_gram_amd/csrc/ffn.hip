@@ -8,7 +8,7 @@
 //   dw_kernel     dWg, dWu, dWd in one launch, k = T, in parts where the tiles alone
 //                 do not fill the chip; dw_reduce_kernel adds the parts in order
 //   tail_kernel   dX and dWg, dWu, dWd in one launch, for few positions
-//   up_few_kernel, down_few_kernel  the forward of up to 32 positions
+//   up_few_kernel, down_few_kernel  the forward of up to 64 positions
 //   dy_kernel     dY' where dY is fp32 or was dropped: a masked copy in bf16
 //
 // Every product is a block tile of mfma_tile.hpp.  Weights are read as they
@@ -655,7 +655,7 @@ __global__ __launch_bounds__(G8::THREADS) void hidden8_kernel(Args a)
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 32 positions: the weights' bytes bound the pass, and the latency of
+// Up to 64 positions: the weights' bytes bound the pass, and the latency of
 // one round of loads most of it.  No LDS stages and no k loop over barriers:
 // every wavefront loads its share of k straight into matrix-core fragments
 // (16 weight rows x 16 positions x 32 values of k each), all loads in flight at
@@ -664,7 +664,9 @@ __global__ __launch_bounds__(G8::THREADS) void hidden8_kernel(Args a)
 // down product has 48 blocks whatever F, so F and T F are bounded: the two
 // meet near T F = 96 Ki (16 x 6144 19 against 19 us, 24 x 4096 16 against 16,
 // 32 x 4096 18 against 16) and, for one position, between F = 8192 (16.5
-// against 20) and 16,384 (29 against 26).
+// against 20) and 16,384 (29 against 26).  From 33 positions on, four tiles of
+// positions: 33 x 424 8.8 against 13.4, 64 x 1000 12.3 against 14.0, but 64 x 2048 17.7
+// against 16.1, so T F is 64 Ki at most there.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
@@ -672,12 +674,13 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-constexpr int kFewT = 32, kFewWaves = 4;
+constexpr int kFewT = 32;   // most positions of wide_rows
+constexpr int kFewWaves = 4;
 constexpr int kFewDown = 8;   // wavefronts of a down block
 
 bool few_rows(int64_t T, int64_t F)
 {
-    return T <= kFewT && F <= 8192 && T * F <= 96 * 1024;
+    return T <= 64 && F <= 8192 && T * F <= (T <= 32 ? 96 : 64) * 1024;
 }
 
 // Calls of few values also keep 16 bits of H, dG and dU, as two bf16 values (the
@@ -1449,7 +1452,7 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     } else if (a.lo) {
         (T > 16 ? launch_few<2, true> : launch_few<1, true>)(a, cfg->act, s);
     } else {
-        (T > 16 ? launch_few<2, false> : launch_few<1, false>)(a, cfg->act, s);
+        (T > 32 ? launch_few<4, false> : T > 16 ? launch_few<2, false> : launch_few<1, false>)(a, cfg->act, s);
     }
     return done();
 }

@@ -115,7 +115,8 @@ def test_whole_numbers_larger(T, F, p):
 
 
 @pytest.mark.parametrize("T,F,p", [(1, 65536, 0.0), (1, 8192, 0.5), (1, 8200, 0.0), (20, 12288, 0.5), (32, 8192, 0.0),
-                                   (12, 8192, 0.5), (13, 8192, 0.0), (4, 2048, 0.5), (4, 2056, 0.0)])
+                                   (12, 8192, 0.5), (13, 8192, 0.0), (4, 2048, 0.5), (4, 2056, 0.0),
+                                   (33, 1984, 0.5), (33, 1992, 0.0), (64, 1024, 0.5), (64, 1032, 0.0), (49, 1336, 0.0)])
 def test_whole_numbers_few_positions(T, F, p):
     # either side of the rules that pick the kernels of few positions and of few values
     _run_whole(T, F, p, max_tokens=T + 3)
