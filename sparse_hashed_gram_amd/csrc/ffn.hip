@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include "../../include/ffn.h"
+#include "ffn_plan.hpp"
 #include "mfma_tile.hpp"
 #include "ngram_dev.hpp"
 #include "philox.hpp"
@@ -27,13 +28,9 @@
 namespace {
 
 using namespace tile;
+using namespace ffn_plan;
 
-constexpr int kD = 768;
-constexpr int kMaxParts = 8;     // parts of k of the weights' gradients
 constexpr uint64_t kAlign = 256;
-constexpr uint32_t kCUs = 256, kXcds = 8;
-
-inline int64_t rup(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // ------------------------------------------------------------- block order
 
@@ -44,8 +41,6 @@ inline int64_t rup(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // 4 / 8 / 16: H 293 / 257 / 257 / 259 us, gradients of the hidden units 543 / 500 /
 // 496 / 542, Y 151 / 149 / 141 / 144, dX 302 / 302 / 300 / 315.
 constexpr uint32_t kGroup = 8;
-
-__host__ __device__ inline uint32_t grid_blocks(uint32_t tiles) { return kXcds * ((tiles + kXcds - 1) / kXcds); }
 
 // rows: tiles of positions, cols: tiles of the other side; block: the block's
 // number, blockIdx.x or, where a block takes several tiles, that plus turns of the grid
@@ -242,6 +237,10 @@ using Half = Shape<2, 1, 2, 2>;     // 128 x 64, 4 wavefronts, three blocks per 
 using Small = Shape<2, 2, 2, 2>;    // 128 x 128, 4 wavefronts, two blocks per CU
 using Mid = Shape<2, 3, 2, 2>;      // 128 x 192, 4 wavefronts, two blocks per CU (81,920 bytes of LDS each)
 using Square = Shape<4, 2, 2, 4>;   // 256 x 256, 8 wavefronts
+
+template <class S>
+constexpr bool is(Size t) { return S::BM == t.bm && S::BN == t.bn; }
+static_assert(is<Half>(kHalf) && is<Small>(kSmall) && is<Mid>(kMid) && is<Square>(kSquare) && kStep == kBK, "ffn_plan.hpp's tiles");
 
 struct Args {
     const uint16_t *X, *Wg, *Wu, *Wd, *dY;
@@ -674,25 +673,8 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-constexpr int kFewT = 32;   // most positions of wide_rows
 constexpr int kFewWaves = 4;
 constexpr int kFewDown = 8;   // wavefronts of a down block
-
-bool few_rows(int64_t T, int64_t F)
-{
-    return T <= 64 && F <= 8192 && T * F <= (T <= 32 ? 96 : 64) * 1024;
-}
-
-// Calls of few values also keep 16 bits of H, dG and dU, as two bf16 values (the
-// rounded one and what that left): with few values behind an output, a rounding
-// that makes its error 1.4 times that of its own rounding alone makes it up to 1.9
-// times in some calls.  Kernels of the forward at 1 x 2048 7.8 -> 9 us (a call is the
-// host's 10.7), of the backward at 1 x 424 19 -> 20; for more values the roundings
-// average out and the products would double.
-bool wide_rows(int64_t T, int64_t F)
-{
-    return T <= kFewT && T * F <= 8192;
-}
 
 // H of 16 hidden units, NT tiles of 16 positions; a wavefront takes a quarter of k.
 template <int ACT, int NT, bool WIDE>
@@ -983,164 +965,6 @@ struct Layout {
     uint64_t S, dY, part, total;
 };
 
-// ---- which tile, and how many parts of k
-//
-// Time of a launch in us, besides 2.5 that all have: turns(blocks) x (step x
-// steps of 64 k + rest), and for parts their sums' way through memory and the
-// launch that adds them.  turns(): a block alone on its CU is bound by latency,
-// a second one fits beside it for a third more, and from about five on the
-// CU's load path (see mfma_tile.hpp) makes them add up.  The constants are
-// measured (T = 30 ... 49,152, F = 128 ... 8000, warm, one process; over 93 pairs
-// of T and F the chosen launches take 1.00 (H and its gradients), 1.01 (Y) and 1.02
-// times (dX and the weights' gradients) the best ones' time):
-//   a step of rows: Half 0.45 - 0.5, Small 0.62, Mid 0.80 us; of dW: Small 0.47, Square 1.47 us;
-//   up (12 steps and epilogue): Half 4.2, Small 7.75, hidden8 22 us a block;
-//   grad (24 steps and epilogue): Half 7.6 (8.6 past two a CU), Small 14.5, hidden8 40 us a block.
-// E.g. T = 1024, F = 2048: up 10.5 / 10.3 / 24 us (Half / Small / hidden8), T =
-// 49,152: Small 371, hidden8 263 us; grad at T = 100: 11.4 / 15.3 us (Half /
-// Small), T = 49,152: Small 620, hidden8 503 us; down at T = 49,152: Small 167,
-// Mid 146 us; dW at T = 1024: Small 19.5, Square 28 us, at T = 49,152: Small
-// 532 (7 parts), Square 451 us (7 parts) against 1,132 (1 part).
-constexpr double kBytesPerUs = 4.5e6;
-constexpr int kMaxRowParts = 16;   // of a [T][768] result
-
-double rounds(int64_t blocks) { return (double)((blocks + kCUs - 1) / kCUs); }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-double turns(int64_t blocks)
-{
-    static const double few[] = {1.0, 1.0, 1.3, 2.0, 2.9};
-    const int64_t r = (blocks + kCUs - 1) / kCUs;
-    return r < 5 ? few[r] : 0.93 * (double)r;
-}
-
-// the parts of a [T][768] result, written, read and added in a launch of their own
-double reduce_us(int64_t T, int p) { return 3.0 + 0.1 * p + p * T * (2.0 * 4 * kD) / kBytesPerUs; }
-
-struct Choice {
-    int shape, parts;   // index into the candidates
-    double us;
-};
-
-void consider(Choice &best, int shape, int parts, double us)
-{
-    if (best.parts == 0 || us < best.us)
-        best = Choice{shape, parts, us};
-}
-
-// Tiles of positions x units; 0 Half, 1 Small, 2 hidden8_kernel's.  A second
-// Half block on a CU costs less than the first, a chip full of Small ones more
-// than a few (gradients, T = 1800, F = 1000: Half, 464 blocks, 19 us, Small, 240, 22; T =
-// 4000, F = 264: 315 blocks 15, 160 blocks 20).
-Choice choose_hidden(int64_t T, int64_t F, bool bwd)
-{
-    Choice c{};
-    auto tiles = [&](int bn, int bm) { return ceil_div(T, bn) * ceil_div(F, bm / 2); };
-    const int64_t half = tiles(Half::BN, Half::BM), small = tiles(Small::BN, Small::BM);
-    const double h = (double)half / kCUs, m = (double)small / kCUs;
-    consider(c, 0, 1, h <= 2.0 ? (bwd ? 7.6 : 4.2) * (h > 1.0 ? 1.2 + 0.4 * h : 1.0) : (bwd ? 8.6 : 4.2) * rounds(half));
-    consider(c, 1, 1, (bwd ? 14.5 : 7.75) * (m <= 1.0 ? 1.0 + 0.3 * m : rounds(small)));
-    if (T >= G8::BN && F >= G8::BM / 2)
-        consider(c, 2, 1, (bwd ? 40.0 : 22.0) * rounds(tiles(G8::BN, G8::BM)));
-    return c;
-}
-
-// Tiles of the three weights' gradients.
-int64_t dw_tiles(int64_t F, int64_t Fp, int bm, int bn)
-{
-    return ceil_div(2 * Fp, bn) * (kD / bm) + (kD / bn) * ceil_div(F, bm);
-}
-
-// A step of Small tiles of the weights' gradients.  Where the operands exceed
-// the L2s, a block alone on its CU waits for them (T = 15,000, F = 400: 198 blocks
-// 0.74 us a step, 462 blocks 0.5).
-double dw_step(int64_t T, int64_t Fp, int64_t blocks)
-{
-    return T * (2 * kD + 6 * Fp) <= (32 << 20) ? 0.47 : blocks <= kCUs ? 0.74 : 0.57;
-}
-
-// A [T][768] result over `steps` stages of k; 0 Half, 1 Small, 2 Mid.  A part
-// has at least two stages, and parts only where a round of blocks holds them.
-// step: 1.4 where the weights' rows are not whole 128-byte lines, else 1; many
-// blocks feel it (Y at T = 3001: F = 2048 23 us, F = 2056 29 us), but not two Small
-// ones on a CU (T = 4000, F = 4104: 1 part 55 us, 2 parts 45).
-Choice choose_rows(int64_t T, int64_t steps, double step)
-{
-    Choice c{};
-    for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
-        const double add = p > 1 ? reduce_us(T, p) : 0.0;
-        const double n = (double)ceil_div(steps, p);
-        const int64_t half = ceil_div(T, Half::BN) * (kD / Half::BM) * p, small = ceil_div(T, Small::BN) * (kD / Small::BM) * p;
-        if (p == 1 || half <= 2 * kCUs)
-            consider(c, 0, p, turns(half) * ((2 * half > kCUs ? 0.45 * step : 0.5) * n + 1.0) + add);
-        if (p == 1 || small <= 2 * kCUs)
-            consider(c, 1, p, turns(small) * (0.62 * (2 * small > kCUs && small <= kCUs ? step : 1.0) * n + 2.0) + add);
-        if (p == 1)
-            consider(c, 2, p, turns(ceil_div(T, Mid::BN) * (kD / Mid::BM)) * (0.80 * n + 2.0));
-    }
-    return c;
-}
-
-// dX and the weights' gradients in one launch, dX on Half or Small tiles: two
-// blocks fit on a CU, and dX's are dispatched first.  While not all are resident
-// the CUs' work adds up; what is left then is a launch of its own, in which a
-// block that shares its CU takes about half as long again (T = 4096, F = 2048,
-// 480 blocks: 67 us expected, 70 measured; 6,000 x 2048, 570: 137 / 131; 6,000 x
-// 4104, 870: 198 / 199; 2,500 x 1000, 264: 32 / 35).
-Choice choose_tail(int64_t T, int64_t F, int64_t Fp)
-{
-    Choice c{};
-    const int64_t steps = 2 * Fp / kBK, dn = grid_blocks((uint32_t)dw_tiles(F, Fp, Small::BM, Small::BN)), slots = 2 * kCUs;
-    const double dt = 0.47 * ceil_div(T, kBK) + 1.3;
-    auto one = [&](int shape, int p, int64_t tiles, double t) {
-        const int64_t n = grid_blocks((uint32_t)(tiles * p));   // slots are an XCD's: whole eighths
-        if (p > 1 && n > slots)
-            return;
-        const double add = p > 1 ? reduce_us(T, p) : 0.0;
-        double us = 0.0;
-        int64_t x = n, w = dn;   // blocks left
-        while (x + w > slots) {
-            const int64_t xs = x < slots ? x : slots, ws = slots - xs;
-            us += (xs * t + ws * dt) / kCUs;
-            x -= xs;
-            w -= ws;
-        }
-        const double last = x && t > dt ? t : dt, sum = (x * t + w * dt) / kCUs;
-        const double alone = (x + w <= kCUs ? 1.1 : 1.45) * last, longest = (n + dn <= kCUs ? 1.1 : 1.45) * t;
-        us += sum > alone ? sum : alone;
-        consider(c, shape, p, add + (us > longest ? us : longest));
-    };
-    for (int p = 1; p <= kMaxRowParts && (p == 1 || 2 * p <= steps); ++p) {
-        const double n = (double)ceil_div(steps, p);
-        one(0, p, ceil_div(T, Half::BN) * (kD / Half::BM), 0.5 * n + 1.0);
-        one(1, p, ceil_div(T, Small::BN) * (kD / Small::BM), 0.62 * n + 2.0);
-    }
-    return c;
-}
-
-// The most bytes the parts' sums take for any T up to max_tokens: with parts a
-// result has at most 2 kCUs blocks of 128 x 128.
-uint64_t row_part_bytes(int64_t max_tokens)
-{
-    const uint64_t all = 2ull * kCUs * Small::BM * Small::BN * 4, few = 4ull * kMaxRowParts * max_tokens * kD;
-    return all < few ? all : few;
-}
-
-// The weights' gradients; 0 Small, 1 Square.
-Choice choose_dw(int64_t T, int64_t F, int64_t Fp)
-{
-    Choice c{};
-    const int64_t steps = ceil_div(T, kBK);
-    for (int p = 1; p <= kMaxParts && p <= steps; ++p) {
-        const double add = p > 1 ? 3.0 + p * Fp * (2.0 * 4 * 3 * kD) / kBytesPerUs : 0.0, n = (double)ceil_div(steps, p);
-        const int64_t small = p * dw_tiles(F, Fp, Small::BM, Small::BN);
-        consider(c, 0, p, rounds(small) * (dw_step(T, Fp, small) * n + 1.3) + add);
-        consider(c, 1, p, rounds(p * dw_tiles(F, Fp, Square::BM, Square::BN)) * (1.47 * n + 3.5) + add);
-    }
-    return c;
-}
-
 Layout layout(const ffn_config *c, int pass)
 {
     Layout L{};
@@ -1295,35 +1119,31 @@ void launch_tail(Args a, int parts, DwArgs d, hipStream_t s)
     reduce_rows<true>(a, s);
 }
 
-void up(const Args &a, int act, hipStream_t s)
+void up(const Args &a, const Choice &c, int act, hipStream_t s)
 {
-    const Choice c = choose_hidden(a.T, a.F, false);
     (c.shape == 0 ? launch_up<Half> : c.shape == 1 ? launch_up<Small> : launch_hidden8<false>)(a, act, s);
 }
 
-void grad(const Args &a, int act, hipStream_t s)
+void grad(const Args &a, const Choice &c, int act, hipStream_t s)
 {
-    const Choice c = choose_hidden(a.T, a.F, true);
     (c.shape == 0 ? launch_grad<Half> : c.shape == 1 ? launch_grad<Small> : launch_hidden8<true>)(a, act, s);
 }
 
 template <bool DX>
-void rows(const Args &a, hipStream_t s)
+void rows(const Args &a, const Choice &c, hipStream_t s)
 {
-    const Choice c = choose_rows(a.T, (DX ? 2 : 1) * a.Fp / kBK, !DX && a.F % kBK ? 1.4 : 1.0);
     (c.shape == 0 ? launch_rows<Half, DX> : c.shape == 1 ? launch_rows<Small, DX> : launch_rows<Mid, DX>)(a, c.parts, s);
 }
 
 // dX and the weights' gradients
-void tail(const Args &a, const DwArgs &d, hipStream_t s)
+void tail(const Args &a, const DwArgs &d, const Bwd &p, hipStream_t s)
 {
-    const Choice both = choose_tail(a.T, a.F, a.Fp), x = choose_rows(a.T, 2 * a.Fp / kBK, 1.0), w = choose_dw(a.T, a.F, a.Fp);
-    if (a.lo || both.us < x.us + w.us + 2.5) {
-        (both.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, both.parts, d, s);
+    if (p.merged) {
+        (p.rows.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, p.rows.parts, d, s);
         return;
     }
-    rows<true>(a, s);
-    (w.shape == 0 ? launch_dw<Small> : launch_dw<Square>)(d, w.parts, s);
+    rows<true>(a, p.rows, s);
+    (p.dw.shape == 0 ? launch_dw<Small> : launch_dw<Square>)(d, p.dw.parts, s);
 }
 
 }   // namespace
@@ -1444,11 +1264,12 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     a.out = Y;
     a.out_f32 = cfg->y_dtype == FFN_DTYPE_F32;
     hipStream_t s = (hipStream_t)stream;
-    if (wide_rows(T, a.F))
+    const Fwd p = plan_fwd(T, a.F);
+    if (p.wide)
         a.lo = (uint16_t *)a.part;   // 2 T Fp <= 16,384 T bytes; part holds 49,152 T
-    if (!few_rows(T, a.F)) {
-        up(a, cfg->act, s);
-        rows<false>(a, s);
+    if (!p.few) {
+        up(a, p.hidden, cfg->act, s);
+        rows<false>(a, p.rows, s);
     } else if (a.lo) {
         (T > 16 ? launch_few<2, true> : launch_few<1, true>)(a, cfg->act, s);
     } else {
@@ -1513,14 +1334,15 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     d.S = a.S;
     d.scale = a.mask.scale;
     d.part = (float *)((uint8_t *)ws + L.part);
-    if (wide_rows(T, a.F)) {
+    const Bwd p = plan_bwd(T, a.F);
+    if (p.wide) {
         // behind the parts of dX; the whole is at least 73,728 Fp bytes
         static_assert(kMaxRowParts * kFewT * kD * 4 + 6 * kFewT * 64 <= 4 * kMaxParts * 3 * kD * 64, "room at Fp = 64");
         a.lo = (uint16_t *)(a.part + kMaxRowParts * kFewT * kD);
         d.lo = a.lo;
     }
-    grad(a, cfg->act, s);
-    tail(a, d, s);
+    grad(a, p.hidden, cfg->act, s);
+    tail(a, d, p, s);
     return done();
 }
 

@@ -1,0 +1,81 @@
+"""Which kernels the GPU tests of the feed-forward block reach, checked on the
+CPU: csrc/ffn_plan.hpp, the rules that pick them, is compiled here
+(tests/kernel_model/ffn_plan.cpp), and every kernel, tile and form of joining
+that some size takes has to be taken by a size that a parity test runs."""
+import ctypes
+import itertools
+import math
+import os
+import random
+import subprocess
+
+import pytest
+
+import test_gpu_ffn
+import test_gpu_ffn_tiles
+
+SRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "kernel_model", "ffn_plan.cpp")
+HIDDEN = ("128 x 64", "128 x 128", "hidden8")
+ROWS = ("128 x 64", "128 x 128", "128 x 192")
+DW = ("128 x 128", "256 x 256")
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    lib = str(tmp_path_factory.mktemp("plan") / "libplan.so")
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", SRC, "-o", lib])
+    L = ctypes.CDLL(lib)
+    L.model_plan.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]
+    L.model_plan.restype = None
+    f, b = (ctypes.c_int32 * 5)(), (ctypes.c_int32 * 7)()
+
+    def kernels(T, F):
+        """What a forward and a backward of T positions and F hidden units launch."""
+        L.model_plan(T, F, f, b)
+        few, wide, hidden, rows, parts = f
+        if few:
+            out = {("few", 1 if T <= 16 else 2 if T <= 32 else 4, "two bf16" if wide else "one bf16")}
+        else:
+            out = {("H", HIDDEN[hidden]), ("Y", ROWS[rows], "parts" if parts > 1 else "whole")}
+        wide, merged, hidden, rows, parts, dw, dw_parts = b
+        out.add(("hidden gradients", HIDDEN[hidden], "two bf16" if wide else "one bf16"))
+        how = "parts" if parts > 1 else "whole"
+        if merged:
+            out.add(("dX with the weights' gradients", ROWS[rows], how, "two bf16" if wide else "one bf16"))
+        else:
+            out |= {("dX", ROWS[rows], how), ("weights' gradients", DW[dw], "parts" if dw_parts > 1 else "whole")}
+        return out
+
+    return kernels
+
+
+def _sizes(module):
+    """(T, F) of every case that the module's parametrised tests run."""
+    for name, f in vars(module).items():
+        marks = [m for m in getattr(f, "pytestmark", []) if m.name == "parametrize"] if name.startswith("test_") else []
+        if not marks:
+            continue
+        for values in itertools.product(*(m.args[1] for m in marks)):
+            case = {}
+            for m, v in zip(marks, values):
+                names = [n.strip() for n in m.args[0].split(",")]
+                case.update(zip(names, v if len(names) > 1 else [v]))
+            if "T" in case and "F" in case:
+                yield case["T"], case["F"]
+
+
+def test_every_kernel_is_reached(plan):
+    r = random.Random(3)
+    spread = lambda hi: int(math.exp(r.uniform(0, math.log(hi + 1))))   # noqa: E731
+    taken = set()
+    for _ in range(40000):
+        taken |= plan(spread(60000), 8 * spread(8192))
+    # sizes of a narrow range that the draws above may pass over
+    for T in range(1, 1500, 7):
+        for F in range(2800, 3060, 20):
+            taken |= plan(T, F // 8 * 8)
+    tested = set()
+    for case in itertools.chain(_sizes(test_gpu_ffn), _sizes(test_gpu_ffn_tiles)):
+        tested |= plan(*case)
+    assert len(taken) > 25
+    assert not taken - tested, f"no parity test reaches {sorted(taken - tested)}"
