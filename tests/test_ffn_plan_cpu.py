@@ -79,3 +79,11 @@ def test_every_kernel_is_reached(plan):
         tested |= plan(*case)
     assert len(taken) > 25
     assert not taken - tested, f"no parity test reaches {sorted(taken - tested)}"
+
+
+def test_real_values_reach_the_kernels_of_many_positions(plan):
+    many = {("H", "hidden8"), ("Y", "128 x 192", "whole"), ("hidden gradients", "hidden8", "one bf16"),
+            ("dX", "128 x 192", "whole"), ("weights' gradients", "256 x 256", "parts")}
+    for kind in ("silu", "gelu"):
+        tested = set().union(*(plan(c[0], c[1]) for c in test_gpu_ffn_tiles.REAL if c[3] == kind))
+        assert not many - tested, kind

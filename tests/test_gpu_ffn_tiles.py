@@ -1,18 +1,47 @@
 """GPU parity of the feed-forward block's kernels of many positions, at sizes
 that reach each of them (tests/test_ffn_plan_cpu.py holds the lists below to
-that).  The cases are whole numbers, so results are exact
-(test_gpu_ffn.py says why).
+that).  Whole-number cases are exact and real-valued ones are held to the
+bounds that stand, with their derivation, at the top of test_gpu_ffn.py.
 """
+import numpy as np
 import pytest
+import torch
 
-from test_gpu_ffn import _run_whole
+from oracle import drop as orcd
+from test_gpu_ffn import D, M, NAMES, _bf16, _bounds, _hold, _real, _run_whole
 
 pytestmark = pytest.mark.gpu
 
 # positions, hidden units, share dropped
 WHOLE = [(8193, 1000, 0.5), (4001, 1000, 0.0), (1100, 2848, 0.5), (617, 13080, 0.0), (1025, 2992, 0.5)]
+# the same for an activation, types of the stream and of the weights' gradients
+REAL = [(7823, 1000, 0.1, "silu", "bf16", "bf16"), (7823, 1000, 0.3, "gelu", "f32", "f32"),
+        (3001, 2056, 0.0, "gelu", "bf16", "f32"), (3001, 2056, 0.2, "silu", "f32", "bf16")]
 
 
 @pytest.mark.parametrize("T,F,p", WHOLE)
 def test_whole_numbers(T, F, p):
     _run_whole(T, F, p)
+
+
+@pytest.mark.parametrize("T,F,p,kind,yt,wt", REAL)
+def test_real_values(T, F, p, kind, yt, wt):
+    m = M()
+    X, W, dY, res = _real(T, F)
+    cfg = m.config(F, T, act=kind, y_dtype=yt, dw_dtype=wt)
+    ws = m.Workspace(cfg)
+    spec = D().spec(p, 5, 6) if p else None
+    factor = orcd.keep(T, 768, p, 5, 6) * (65536 / (65536 - orcd.threshold(p))) if p else None
+    td, b = cfg.y_torch_dtype, 2.0 ** -24
+    Xd, Wc = _bf16(X).cuda(), [_bf16(w).cuda() for w in W]
+    resd, dYd = torch.from_numpy(res).to(td).cuda(), torch.from_numpy(dY).to(td).cuda()
+    o = _bounds(X, W, dY, kind, factor, yt == "f32")
+    y = m.fwd(cfg, ws, Xd, *Wc, residual=resd, drop=spec)
+    _hold(y, o["Y"][0] + res, o["Y"][1] + 2 * b * np.abs(res), yt == "bf16", "Y")
+    g = m.bwd(cfg, ws, Xd, *Wc, dYd, drop=spec)
+    for k in NAMES:
+        _hold(g[k], *o[k], g[k].dtype == torch.bfloat16, k)
+    # and again, over whatever the first pass left in the workspace
+    assert torch.equal(y, m.fwd(cfg, ws, Xd, *Wc, residual=resd, drop=spec))
+    h = m.bwd(cfg, ws, Xd, *Wc, dYd, drop=spec)
+    assert all(torch.equal(g[k], h[k]) for k in NAMES)
