@@ -87,3 +87,11 @@ def test_real_values_reach_the_kernels_of_many_positions(plan):
     for kind in ("silu", "gelu"):
         tested = set().union(*(plan(c[0], c[1]) for c in test_gpu_ffn_tiles.REAL if c[3] == kind))
         assert not many - tested, kind
+
+
+def test_accumulation_reaches_both_ends(plan):
+    tested = set().union(*(plan(c[0], c[1]) for c in test_gpu_ffn_tiles.ACCUM))
+    for tile in DW:
+        assert ("weights' gradients", tile, "parts") in tested
+    assert any(k[0] == "dX with the weights' gradients" for k in tested)
+    assert ("weights' gradients", "256 x 256", "whole") in tested

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from oracle import drop as orcd
-from test_gpu_ffn import D, M, NAMES, _bf16, _bounds, _hold, _real, _run_whole
+from oracle import ffn as orc
+from test_gpu_ffn import D, M, NAMES, _bf16, _bounds, _hold, _real, _run_whole, _same, _whole
 
 pytestmark = pytest.mark.gpu
 
@@ -17,11 +18,39 @@ WHOLE = [(8193, 1000, 0.5), (4001, 1000, 0.0), (1100, 2848, 0.5), (617, 13080, 0
 # the same for an activation, types of the stream and of the weights' gradients
 REAL = [(7823, 1000, 0.1, "silu", "bf16", "bf16"), (7823, 1000, 0.3, "gelu", "f32", "f32"),
         (3001, 2056, 0.0, "gelu", "bf16", "f32"), (3001, 2056, 0.2, "silu", "f32", "bf16")]
+# accumulated weights' gradients: in parts on both tiles, and in one part
+ACCUM = [(8193, 1000, 0.5), (3500, 264, 0.0), (333, 520, 0.5), (300, 65536, 0.0)]
 
 
 @pytest.mark.parametrize("T,F,p", WHOLE)
 def test_whole_numbers(T, F, p):
     _run_whole(T, F, p)
+
+
+@pytest.mark.parametrize("dw", ["f32", "bf16"])
+@pytest.mark.parametrize("T,F,p", ACCUM)
+def test_accumulated_gradients(T, F, p, dw):
+    # two micro-steps into gradients that hold whole numbers already.  Every sum is
+    # exact in fp32, so bf16 gradients are the rounded sums, once a micro-step
+    m = M()
+    cfg = m.config(F, T, act="relu2", y_dtype="f32", dw_dtype=dw, accumulate=True)
+    ws = m.Workspace(cfg)
+    td = cfg.dw_torch_dtype
+    r = np.random.default_rng([T, F, 11])
+    want = [torch.from_numpy(r.integers(-3, 4, s)).float().to(td) for s in ((F, 768), (F, 768), (768, F))]
+    got = [w.cuda() for w in want]
+    for step in range(2):
+        X, W, dY, _ = _whole(T, F, 20 + step)
+        spec = D().spec(p, 5, step) if p else None
+        factor = orcd.keep(T, 768, p, 5, step) * 2.0 if p else None
+        g = m.bwd(cfg, ws, _bf16(X).cuda(), *(_bf16(w).cuda() for w in W), torch.from_numpy(dY).float().cuda(), spec,
+                  None, *got)
+        o = orc.backward(X, *W, dY, "relu2", factor)
+        _same(g["dX"], o["dX"], "dX")
+        for i, k in enumerate(NAMES[1:]):
+            want[i] = (want[i].double() + torch.from_numpy(o[k])).float().to(td)
+            assert g[k].data_ptr() == got[i].data_ptr()
+            _same(g[k], want[i].double().numpy(), f"{k} of step {step}")
 
 
 @pytest.mark.parametrize("T,F,p,kind,yt,wt", REAL)
