@@ -74,3 +74,25 @@ def test_real_values(T, F, p, kind, yt, wt):
     assert torch.equal(y, m.fwd(cfg, ws, Xd, *Wc, residual=resd, drop=spec))
     h = m.bwd(cfg, ws, Xd, *Wc, dYd, drop=spec)
     assert all(torch.equal(g[k], h[k]) for k in NAMES)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "relu2"])
+def test_nan_and_inf_stay_in_their_rows(kind):
+    # 7,823 positions: the last tile of 256 is moved back to 7,567, so rows up to
+    # 7,679 are written by two blocks
+    m = M()
+    T, F = 7823, 1000
+    X, W, dY, _ = _real(T, F, 4)
+    Xd, Wc, dYd = _bf16(X).cuda(), [_bf16(w).cuda() for w in W], _bf16(dY).cuda()
+    cfg = m.config(F, T, act=kind)
+    ws = m.Workspace(cfg)
+    clean, cdx = m.fwd(cfg, ws, Xd, *Wc), m.bwd(cfg, ws, Xd, *Wc, dYd)["dX"]
+    rows = torch.tensor([0, 7566, 7567, 7600, 7679, 7680, 7822], device="cuda")
+    bad = Xd.clone()
+    bad[rows, 3] = torch.tensor([float("nan"), float("inf"), float("nan"), float("-inf"), float("nan"), float("inf"),
+                                 float("nan")], dtype=torch.bfloat16, device="cuda")
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[rows] = False
+    y, dx = m.fwd(cfg, ws, bad, *Wc), m.bwd(cfg, ws, bad, *Wc, dYd)["dX"]
+    assert torch.equal(y[rest], clean[rest]) and torch.equal(dx[rest], cdx[rest])
+    assert torch.all(torch.any(~torch.isfinite(y[rows]), 1))
