@@ -138,6 +138,23 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]);
 // What rounding v to bf16 (r) left, itself in bf16: together 16 bits of it.
 __device__ __forceinline__ float left_over(float v, float r) { return isinf(r) ? 0.0f : v - r; }
 
+// The sum of products of rounded values and of what the rounding left (sums of
+// their own): an infinity among the other operands times a left-over of 0 or of
+// the other sign must not undo the infinity that it gave with the value itself.
+__device__ __forceinline__ float with_left(float sum, float left) { return isfinite(sum) ? sum + left : sum; }
+
+template <int WM, int WN>
+__device__ __forceinline__ void add_left(f32x16 (&sum)[WM][WN], const f32x16 (&left)[WM][WN])
+{
+#pragma unroll
+    for (int mb = 0; mb < WM; ++mb)
+#pragma unroll
+        for (int nb = 0; nb < WN; ++nb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                sum[mb][nb][e] = with_left(sum[mb][nb][e], left[mb][nb][e]);
+}
+
 __device__ __forceinline__ uint4 pack8_left(const float (&v)[8], const uint4 &rounded)
 {
     float r[8];
@@ -332,7 +349,8 @@ __device__ __forceinline__ void put_rows(const Args &a, const drop::Key &key, in
 template <class S, bool DX>
 constexpr uint32_t kRowsLds = smem_for<S, S::WM>(S::template smem<DX, false, S::WM>());
 
-template <class S, bool DX>
+// WIDE (see wide_rows): S's left-overs as well.
+template <class S, bool DX, bool WIDE>
 __device__ __forceinline__ void rows_tile(const Args &a, uint32_t block, uint8_t *sm)
 {
     uint32_t tt, ot;
@@ -346,11 +364,15 @@ __device__ __forceinline__ void rows_tile(const Args &a, uint32_t block, uint8_t
     clear(acc);
     if constexpr (DX) {
         const Operand A{{a.Wg, a.Wu}, kD, d0, kD, (int32_t)a.Fp, (int32_t)a.F, 0};
-        for (const uint16_t *from = a.S;; from = a.lo) {
-            const Operand B{{from, from}, 3 * a.Fp, n0, a.T, (int32_t)a.Fp, (int32_t)a.F, 0};
-            S::template run<true, false, S::WM>(A, B, k0, k1 - k0, sm, acc);
-            if (!a.lo || from == a.lo)
-                break;
+        auto from = [&](const uint16_t *src) {
+            return Operand{{src, src}, 3 * a.Fp, n0, a.T, (int32_t)a.Fp, (int32_t)a.F, 0};
+        };
+        S::template run<true, false, S::WM>(A, from(a.S), k0, k1 - k0, sm, acc);
+        if constexpr (WIDE) {
+            f32x16 left[S::WM][S::WN];
+            clear(left);
+            S::template run<true, false, S::WM>(A, from(a.lo), k0, k1 - k0, sm, left);
+            add_left(acc, left);
         }
     } else {
         S::template run<false, false, S::WM>(rows_of(a.Wd, a.F, d0, kD, a.F), rows_of(a.S, a.Fp, n0, a.T, a.F), k0,
@@ -381,7 +403,7 @@ template <class S, bool DX>
 __global__ __launch_bounds__(S::THREADS) void rows_kernel(Args a)
 {
     __shared__ __align__(16) uint8_t sm[kRowsLds<S, DX>];
-    rows_tile<S, DX>(a, blockIdx.x, sm);
+    rows_tile<S, DX, false>(a, blockIdx.x, sm);
 }
 
 // v += the parts' 8 values at i, in order; eight parts' loads at a time are in flight.
@@ -753,7 +775,7 @@ __global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         ph[n] = (16 * n + r < a.T ? 16 * n + r : a.T - 1) * a.Fp;
-    f32x4 acc[NT] = {};
+    f32x4 acc[NT] = {}, left[NT] = {};
     const bf16x8 zero = {};
     for (int64_t k0 = (int64_t)w * 32 + 8 * (lane >> 4); k0 - 8 * (lane >> 4) < a.F; k0 += U * kFewDown * 32) {
         bf16x8 x[U], h[U][NT], l[U][NT];
@@ -775,12 +797,18 @@ __global__ __launch_bounds__(64 * kFewDown) void down_few_kernel(Args a)
             for (int n = 0; n < NT; ++n) {
                 acc[n] = mfma16(x[s], h[s][n], acc[n]);
                 if constexpr (WIDE)
-                    acc[n] = mfma16(x[s], l[s][n], acc[n]);
+                    left[n] = mfma16(x[s], l[s][n], left[n]);
             }
     }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[n][e] = with_left(acc[n][e], left[n][e]);
+        }
         red[w][n][lane] = acc[n];
+    }
     __syncthreads();
     // one thread: 8 outputs of one position, the halves of two lanes of the sums
     const int n = threadIdx.x / 32, q = threadIdx.x % 32;
@@ -833,7 +861,7 @@ __device__ __forceinline__ void put_dw(const DwArgs &a, void *dst, int64_t i, fl
 template <class S>
 constexpr uint32_t kDwLds = smem_for<S, S::WM>(S::template smem<true, true, S::WM>());
 
-template <class S>
+template <class S, bool WIDE>
 __device__ __forceinline__ void dw_tile(const DwArgs &a, uint32_t block, uint8_t *sm)
 {
     const uint32_t first = a.tiles_f2 * a.tiles_d, tiles = first + a.tiles_e * a.tiles_h;
@@ -863,15 +891,18 @@ __device__ __forceinline__ void dw_tile(const DwArgs &a, uint32_t block, uint8_t
                      : rows_of(a.X + k0 * kD, kD, m0, kD, valid);
     Operand B = down ? rows_of(a.dY + k0 * kD, kD, n0, kD, valid)
                      : rows_of(a.S + k0 * ls, ls, n0, 2 * a.Fp, valid);
-    int64_t K = k1 - k0;
-    if (a.lo) {   // one stage of positions: the same again with the left-overs
-        A.seg = B.seg = kBK;
-        (down ? A : B).src[1] = a.lo + (down ? 2 * a.Fp : 0);
-        K = 2 * kBK;
-    }
     f32x16 acc[S::WM][S::WN];
     clear(acc);
-    S::template run<true, true, S::WM>(A, B, 0, K, sm, acc);
+    if constexpr (WIDE) {   // one stage of positions, and the same again with the left-overs
+        A.seg = B.seg = kBK;
+        (down ? A : B).src[1] = a.lo + (down ? 2 * a.Fp : 0);
+        f32x16 left[S::WM][S::WN];
+        clear(left);
+        product_1_1<true, true, S::WM, S::WN, S::GM, S::GN>(A, B, sm, acc, left);
+        add_left(acc, left);
+    } else {
+        S::template run<true, true, S::WM>(A, B, 0, k1 - k0, sm, acc);
+    }
     const int w = threadIdx.x >> 6, wm = w / S::GN, wn = w % S::GN;
     float *lds = reinterpret_cast<float *>(sm + w * Rows<S::WM>::BYTES);
     float *pp = a.parts > 1 ? a.part + part * (3 * a.Fp * kD) : nullptr;
@@ -905,22 +936,22 @@ template <class S>
 __global__ __launch_bounds__(S::THREADS) void dw_kernel(DwArgs a)
 {
     __shared__ __align__(16) uint8_t sm[kDwLds<S>];
-    dw_tile<S>(a, blockIdx.x, sm);
+    dw_tile<S, false>(a, blockIdx.x, sm);
 }
 
 // dX and the weights' gradients in one launch: neither needs the other, and
 // alone neither fills the chip while a backward is short (T = 257, F = 1000: 13.3
 // us against 19.4, T = 4096, F = 2048: 71 against 97; from about 6,000 x 2048 on
 // the larger tiles of dw_kernel win, 8,192 x 2304: 162 against 157).
-template <class S>
+template <class S, bool WIDE>
 __global__ __launch_bounds__(S::THREADS) void tail_kernel(Args a, DwArgs d, uint32_t row_blocks)
 {
     static_assert(S::THREADS == Small::THREADS, "one block size");
     __shared__ __align__(16) uint8_t sm[cmax(kRowsLds<S, true>, kDwLds<Small>)];
     if (blockIdx.x < row_blocks)
-        rows_tile<S, true>(a, blockIdx.x, sm);
+        rows_tile<S, true, WIDE>(a, blockIdx.x, sm);
     else
-        dw_tile<Small>(d, blockIdx.x - row_blocks, sm);
+        dw_tile<Small, WIDE>(d, blockIdx.x - row_blocks, sm);
 }
 
 // The parts of k, added in order; blockIdx.y: dWg, dWu, dWd.  parts = 0 gives
@@ -1111,11 +1142,11 @@ void launch_dw(DwArgs d, int parts, hipStream_t s)
 }
 
 // (with parts of the weights' gradients both sums would lie in one place)
-template <class S>
+template <class S, bool WIDE>
 void launch_tail(Args a, int parts, DwArgs d, hipStream_t s)
 {
     const uint32_t n = set_rows<S>(a, parts), m = set_dw<Small>(d, 1);
-    tail_kernel<S><<<n + m, S::THREADS, 0, s>>>(a, d, n);
+    tail_kernel<S, WIDE><<<n + m, S::THREADS, 0, s>>>(a, d, n);
     reduce_rows<true>(a, s);
 }
 
@@ -1139,7 +1170,9 @@ void rows(const Args &a, const Choice &c, hipStream_t s)
 void tail(const Args &a, const DwArgs &d, const Bwd &p, hipStream_t s)
 {
     if (p.merged) {
-        (p.rows.shape == 0 ? launch_tail<Half> : launch_tail<Small>)(a, p.rows.parts, d, s);
+        // (at most a tile of positions where wide: Small tiles are then as many, and longer)
+        (p.wide ? launch_tail<Half, true> : p.rows.shape == 0 ? launch_tail<Half, false> : launch_tail<Small, false>)(
+            a, p.rows.parts, d, s);
         return;
     }
     rows<true>(a, p.rows, s);

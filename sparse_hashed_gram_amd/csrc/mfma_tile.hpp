@@ -481,6 +481,35 @@ __device__ __forceinline__ void product(const Operand &A, const Operand &B, int3
     __syncthreads();
 }
 
+// Two products of one stage each, the first kBK values of k and the next, into
+// sums of their own; both stages' loads are in flight at once.
+template <bool AK, bool BK, int WM, int WN, int GM, int GN>
+__device__ __forceinline__ void product_1_1(const Operand &A, const Operand &B, uint8_t *sm, f32x16 (&acc1)[WM][WN],
+                                            f32x16 (&acc2)[WM][WN])
+{
+    using T = Tile<AK, BK, WM, WN, GM, GN>;
+    T t;
+    t.init(A, B, 0);
+    lds_u8 *s0, *s1;
+    places(sm, T::STAGE, s0, s1);
+    t.issue(s0);
+    t.issue(s1);
+    wait_vmcnt<0>();
+    barrier_nofence();
+    bf16x8 a[WM], b[WN];
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk) {
+        t.read(s0, kk, a, b);
+        multiply(a, b, acc1);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kBK / 16; ++kk) {
+        t.read(s1, kk, a, b);
+        multiply(a, b, acc2);
+    }
+    __syncthreads();
+}
+
 // Two products over the same K, step by step together.  A step of a small tile is
 // its own chain of LDS reads, dependent matrix instructions and a barrier (0.3
 // us for two instructions a sub-step), so two of them cost little more than one.

@@ -95,3 +95,13 @@ def test_accumulation_reaches_both_ends(plan):
         assert ("weights' gradients", tile, "parts") in tested
     assert any(k[0] == "dX with the weights' gradients" for k in tested)
     assert ("weights' gradients", "256 x 256", "whole") in tested
+
+
+def test_calls_of_few_values_take_the_kernels_they_are_launched_on(plan):
+    # ffn.hip launches one form of each for them, whatever the plan's tile
+    for T in range(1, 65):
+        for F in range(8, 8192 // T + 1, 8):
+            for k in plan(T, F):
+                if k[-1] == "two bf16":
+                    assert k[0] in ("few", "hidden gradients") or k[:2] == ("dX with the weights' gradients", "128 x 64"), k
+                    assert k[0] != "hidden gradients" or k[1] == "128 x 64"
