@@ -17,9 +17,12 @@
  * Precision: products of bf16 values on the matrix cores, summed in fp32;
  * the activation and its derivative in fp32 from the fp32 sums.  Rounded to
  * bf16 (nearest, ties to even) on the way, each once and only because it is an
- * operand of a further product: H, dG and dU, and dY where it is fp32.  (Calls
- * of at most 32 positions and T F <= 8192 keep 16 bits of H, dG and dU, as two bf16
- * values: so few roundings need not average out.)  The
+ * operand of a further product: H, dG and dU, and dY where it is fp32.  Each
+ * makes a result's error about sqrt(2) times that of its own rounding; calls of
+ * at most 64 positions and T F <= 8192, where a call's error strays far from that
+ * average, keep 16 bits of H, dG and dU (not of an fp32 dY), as two bf16 values.
+ * So a position's result may differ in its last bits with the number of
+ * positions in its call.  The
  * scale of the dropout is applied to fp32 sums.  Y, dX and the weights'
  * gradients are rounded once, at the end.  The backward computes G and U
  * again from X: the forward keeps nothing, which saves 4 T F bytes of

@@ -680,9 +680,9 @@ __global__ __launch_bounds__(G8::THREADS) void hidden8_kernel(Args a)
 // one round of loads most of it.  No LDS stages and no k loop over barriers:
 // every wavefront loads its share of k straight into matrix-core fragments
 // (16 weight rows x 16 positions x 32 values of k each), all loads in flight at
-// once, and the wavefronts' sums meet in LDS.  F = 2048: T = 1 7.9 us against
-// 14.5 through the tiles, T = 16 10 against 15, T = 32 12.7 against 15.5.  The
-// down product has 48 blocks whatever F, so F and T F are bounded: the two
+// once, and the wavefronts' sums meet in LDS.  F = 2048: T = 1 7.9 us (8.5 with
+// two bf16 values of H) against 14.5 through the tiles, T = 16 10 against 15, T =
+// 32 12.7 against 15.5.  The down product has 48 blocks whatever F, so F and T F are bounded: the two
 // meet near T F = 96 Ki (16 x 6144 19 against 19 us, 24 x 4096 16 against 16,
 // 32 x 4096 18 against 16) and, for one position, between F = 8192 (16.5
 // against 20) and 16,384 (29 against 26).  From 33 positions on, four tiles of
@@ -1304,7 +1304,7 @@ int ffn_fwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
         up(a, p.hidden, cfg->act, s);
         rows<false>(a, p.rows, s);
     } else if (a.lo) {
-        (T > 16 ? launch_few<2, true> : launch_few<1, true>)(a, cfg->act, s);
+        (T > 32 ? launch_few<4, true> : T > 16 ? launch_few<2, true> : launch_few<1, true>)(a, cfg->act, s);
     } else {
         (T > 32 ? launch_few<4, false> : T > 16 ? launch_few<2, false> : launch_few<1, false>)(a, cfg->act, s);
     }

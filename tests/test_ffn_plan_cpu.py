@@ -12,6 +12,7 @@ import subprocess
 import pytest
 
 import test_gpu_ffn
+import test_gpu_ffn_few
 import test_gpu_ffn_tiles
 
 SRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "kernel_model", "ffn_plan.cpp")
@@ -75,7 +76,7 @@ def test_every_kernel_is_reached(plan):
         for F in range(2800, 3060, 20):
             taken |= plan(T, F // 8 * 8)
     tested = set()
-    for case in itertools.chain(_sizes(test_gpu_ffn), _sizes(test_gpu_ffn_tiles)):
+    for case in itertools.chain(_sizes(test_gpu_ffn), _sizes(test_gpu_ffn_few), _sizes(test_gpu_ffn_tiles)):
         tested |= plan(*case)
     assert len(taken) > 25
     assert not taken - tested, f"no parity test reaches {sorted(taken - tested)}"
