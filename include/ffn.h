@@ -91,9 +91,9 @@ int ffn_config_check(const ffn_config *cfg);
 
 /* Bytes of workspace that a pass of cfg needs (host output `bytes`); one of
  * the backward's size serves both.  About 2 T F bytes for the forward and
- * 6 T F + 1536 T + 73,728 F for the backward, T the config's max_tokens, and
- * for parts of k of small calls at most 33.6 MB (in the backward: shared with
- * the 73,728 F). */
+ * 6 T F + 1536 T for the backward, T the config's max_tokens, and room for parts
+ * of k: 49,152 T, at most 33.6 MB; in the backward, where it is more and T is
+ * over 64, 9,216 F for each 64 of T, at most 73,728 F. */
 int ffn_workspace_bytes(const ffn_config *cfg, int pass, uint64_t *bytes);
 
 /* Forward.  ws: ws_bytes bytes, at least what FFN_PASS_FWD needs, 256-byte

@@ -19,6 +19,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/ffn.h"
 #include "ffn_plan.hpp"
 #include "mfma_tile.hpp"
@@ -1010,8 +1012,10 @@ Layout layout(const ffn_config *c, int pass)
     if (pass == FFN_PASS_BWD) {
         L.dY = take(2ull * c->max_tokens * kD);
     }
-    const uint64_t rows = row_part_bytes(c->max_tokens), dw = 4ull * kMaxParts * 3 * L.Fp * kD;
-    L.part = take(pass == FFN_PASS_BWD && dw > rows ? dw : rows);
+    uint64_t part = row_part_bytes(c->max_tokens);
+    if (pass == FFN_PASS_BWD)
+        part = std::max({part, dw_part_bytes(c->max_tokens, L.Fp), wide_bytes(c->max_tokens, c->hidden, L.Fp)});
+    L.part = take(part);
     L.total = o;
     return L;
 }
@@ -1369,9 +1373,7 @@ int ffn_bwd(const ffn_config *cfg, void *ws, uint64_t ws_bytes, const void *X, c
     d.part = (float *)((uint8_t *)ws + L.part);
     const Bwd p = plan_bwd(T, a.F);
     if (p.wide) {
-        // behind the parts of dX; the whole is at least 73,728 Fp bytes
-        static_assert(kMaxRowParts * kFewT * kD * 4 + 6 * kFewT * 64 <= 4 * kMaxParts * 3 * kD * 64, "room at Fp = 64");
-        a.lo = (uint16_t *)(a.part + kMaxRowParts * kFewT * kD);
+        a.lo = (uint16_t *)(a.part + kMaxRowParts * T * kD);   // behind the parts of dX: wide_bytes
         d.lo = a.lo;
     }
     grad(a, p.hidden, cfg->act, s);

@@ -45,9 +45,11 @@ constexpr int kFewT = 64;   // most positions of wide_rows: one stage of the wei
 // In a captured graph: forward of 1 x 2048 7.9 -> 8.5 us, 32 x 256 7.7 -> 8.4, 64 x 128
 // 9.2 -> 10.1; backward of 1 x 424 19.8 -> 20.9, 1 x 2048 22.0 -> 23.8, 32 x 256 20.4 ->
 // 26.0, 64 x 128 18.8 -> 21.9.  For larger calls the products would double.
+constexpr int64_t kFewValues = 8192;
+
 inline bool wide_rows(int64_t T, int64_t F)
 {
-    return T <= kFewT && T * F <= 8192;
+    return T <= kFewT && T * F <= kFewValues;
 }
 
 // ---- which tile, and how many parts of k
@@ -190,6 +192,22 @@ inline uint64_t row_part_bytes(int64_t max_tokens)
 {
     const uint64_t all = 2ull * kCUs * kSmall.bm * kSmall.bn * 4, few = 4ull * kMaxRowParts * max_tokens * kD;
     return all < few ? all : few;
+}
+
+// The same for the weights' gradients.
+inline uint64_t dw_part_bytes(int64_t max_tokens, int64_t Fp)
+{
+    const int64_t steps = ceil_div(max_tokens, kStep), parts = steps < kMaxParts ? steps : kMaxParts;
+    return parts > 1 ? 4ull * parts * 3 * Fp * kD : 0;
+}
+
+// What calls of wide_rows keep there in the backward: the parts of dX, then the left-overs.
+inline uint64_t wide_bytes(int64_t max_tokens, int64_t F, int64_t Fp)
+{
+    int64_t most = kFewValues / F;   // positions
+    most = most < kFewT ? most : kFewT;
+    most = most < max_tokens ? most : max_tokens;
+    return most * (4ull * kMaxRowParts * kD + 6ull * Fp);
 }
 
 // The weights' gradients; 0 Small, 1 Square.

@@ -30,9 +30,11 @@ def plan(tmp_path_factory):
     L.model_plan.restype = None
     f, b = (ctypes.c_int32 * 5)(), (ctypes.c_int32 * 7)()
 
-    def kernels(T, F):
+    def kernels(T, F, numbers=False):
         """What a forward and a backward of T positions and F hidden units launch."""
         L.model_plan(T, F, f, b)
+        if numbers:
+            return list(f), list(b)
         few, wide, hidden, rows, parts = f
         if few:
             out = {("few", 1 if T <= 16 else 2 if T <= 32 else 4, "two bf16" if wide else "one bf16")}
@@ -48,6 +50,37 @@ def plan(tmp_path_factory):
         return out
 
     return kernels
+
+
+def test_workspace_holds_what_its_calls_take(plan):
+    # bytes of a config's workspace, and of what a call of up to its positions keeps there
+    from sparse_hashed_gram_amd import ffn
+    up = lambda n: -(-n // 256) * 256   # noqa: E731
+    for F in (8, 128, 1000, 2048, 8192, 8200, 65536):
+        Fp = -(-F // 64) * 64
+        for T in (1, 2, 40, 64, 65, 128, 300, 512, 513, 4096, 49152):
+            cfg = ffn.config(F, T)
+            rows = min(16 * 768 * 4 * T, 2 * 256 * 128 * 128 * 4)
+            parts = min(8, -(-T // 64))
+            few = min(T, 64, 8192 // F) * (16 * 768 * 4 + 6 * Fp)
+            part = max(rows, parts * 3 * Fp * 768 * 4 if parts > 1 else 0, few)
+            assert ffn.workspace_bytes(cfg, False) == up(2 * T * Fp) + up(rows)
+            assert ffn.workspace_bytes(cfg) == up(6 * T * Fp) + up(1536 * T) + up(part)
+    assert ffn.workspace_bytes(ffn.config(8192, 1)) < 200_000   # one position needs no parts of the weights' gradients
+    r = random.Random(4)
+    spread = lambda hi: int(math.exp(r.uniform(0, math.log(hi + 1))))   # noqa: E731
+    for _ in range(4000):
+        T, F = spread(60000), 8 * spread(8192)
+        Fp = -(-F // 64) * 64
+        for most in (T, T + 1 + spread(4000)):
+            cfg = ffn.config(F, most)
+            fwd = ffn.workspace_bytes(cfg, False) - 2 * most * Fp
+            bwd = ffn.workspace_bytes(cfg) - 6 * most * Fp - 1536 * most
+            (few, wide, _, _, parts), (_, merged, _, _, rows, _, dw) = plan(T, F, numbers=True)
+            assert fwd >= (2 * T * Fp if wide else 0 if few or parts == 1 else parts * T * 768 * 4)
+            assert bwd >= (16 * T * 768 * 4 + 6 * T * Fp if wide else rows * T * 768 * 4 if rows > 1 else 0)
+            assert rows <= 16
+            assert dw == 1 or (not merged and bwd >= dw * 3 * Fp * 768 * 4)
 
 
 def _sizes(module):

@@ -80,3 +80,27 @@ def test_one_rounding_up_to_64_positions(T, F, kind):
 @pytest.mark.parametrize("T,F,p", [(33, 248, 0.5), (33, 256, 0.0), (64, 128, 0.5), (64, 136, 0.0), (65, 120, 0.5), (50, 8, 0.0)])
 def test_whole_numbers_either_side(T, F, p):
     _run_whole(T, F, p, max_tokens=T + 2)
+
+
+@pytest.mark.parametrize("T,F", [(1, 8192), (1, 8), (64, 128), (31, 264), (65, 1000), (130, 8), (300, 2056)])
+def test_nothing_behind_the_workspace(T, F):
+    # a workspace of exactly the bytes asked for, guarded; results as with a roomy one
+    m = M()
+    X, W, dY, _ = _real(T, F, 80)
+    Xd, Wc, dYd = _bf16(X).cuda(), [_bf16(w).cuda() for w in W], _bf16(dY).cuda()
+    roomy = m.config(F, T + 1000)
+    want = m.bwd(roomy, m.Workspace(roomy), Xd, *Wc, dYd)
+    wy = m.fwd(roomy, m.Workspace(roomy), Xd, *Wc)
+    cfg = m.config(F, T)
+    for backward in (False, True):
+        n = m.workspace_bytes(cfg, backward)
+        buf = torch.full((n + (1 << 20) + 256,), 165, dtype=torch.uint8, device="cuda")
+        off = -buf.data_ptr() % 256
+        ws = m.Workspace(cfg, backward=backward)
+        ws.tensor = buf[off:off + n]
+        ws.ptr = ws.tensor.data_ptr()
+        assert torch.equal(m.fwd(cfg, ws, Xd, *Wc), wy)
+        if backward:
+            got = m.bwd(cfg, ws, Xd, *Wc, dYd)
+            assert all(torch.equal(got[k], want[k]) for k in NAMES)
+        assert torch.all(buf[:off] == 165) and torch.all(buf[off + n:] == 165)
