@@ -65,8 +65,6 @@
 
 #include <stdint.h>
 
-#include "drop.h"
-
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -238,10 +236,14 @@ int ngram_embed_fwd(const ngram_config *cfg, const void *W_b, const void *W_t,
  * a NaN stays a NaN).  Arguments, options and flags as for ngram_embed_fwd.
  * Its backward is drop_bwd of dY under the same spec and shape (in place, if
  * the caller likes), then the calls below with the result.  A bad spec gives
- * NGRAM_ENULL, NGRAM_EARG or NGRAM_EALIGN. */
+ * NGRAM_ENULL, NGRAM_EARG or NGRAM_EALIGN.  Its callers include drop.h, and a
+ * library that has it is told by drop.h's version: it came with
+ * DROP_ABI_VERSION 1 (drop_abi_version is exported), while NGRAM_ABI_VERSION
+ * counts the rest of this header. */
+struct drop_spec;
 int ngram_embed_fwd_drop(const ngram_config *cfg, const void *W_b,
                          const void *W_t, const int32_t *tokens, int64_t T,
-                         const drop_spec *spec, void *out, void *ws,
+                         const struct drop_spec *spec, void *out, void *ws,
                          void *stream);
 
 /* Backward of one micro-step into the window accumulator (gradients are
