@@ -320,7 +320,9 @@ int ngram_embed_fwd_drop(const ngram_config *cfg, const void *W_b, const void *W
         return NGRAM_EALIGN;
     const uintptr_t o = (uintptr_t)out, g = (uintptr_t)spec->rng;
     const uint64_t n = (uint64_t)T * kDim * (cfg->dtype == NGRAM_DTYPE_BF16 && !(cfg->options & NGRAM_OPT_OUT_F32) ? 2 : 4);
-    if (g && g < o + n && o < g + sizeof(drop_rng))   // read by every block, after others wrote
+    // read by every block, after others wrote: results, or a flag in the workspace's header
+    auto meets = [g](uintptr_t p, uint64_t bytes) { return g < p + bytes && p < g + sizeof(drop_rng); };
+    if (g && (meets(o, n) || (ws && meets((uintptr_t)ws, sizeof(WsHeader)))))
         return NGRAM_EARG;
     return hip_status(launch_fwd_drop(cfg->dtype, (cfg->options & NGRAM_OPT_OUT_F32) != 0, hash_params(cfg), W_b,
                                       W_t, tokens, T, *spec, out, flags_of(ws), (hipStream_t)stream));
