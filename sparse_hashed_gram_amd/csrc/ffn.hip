@@ -237,7 +237,6 @@ template <int WM_, int WN_, int GM_, int GN_>
 struct Shape {
     static constexpr int WM = WM_, WN = WN_, GM = GM_, GN = GN_, NW = GM * GN, THREADS = 64 * NW;
     static constexpr int BM = 32 * WM * GM, BN = 32 * WN * GN;
-    static constexpr bool BIG = NW == 8;
 
     template <bool AK, bool BK, int M>
     static constexpr uint32_t smem()
