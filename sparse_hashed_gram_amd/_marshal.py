@@ -1,9 +1,12 @@
-"""Checks of tensors and the stream of a call, shared by the bindings of
-``drop``, ``ffn`` and ``ngram.embed_fwd_drop``.
+"""Loading of the library, shared by the bindings, and the checks of tensors and
+the stream of a call of ``drop``, ``ffn`` and ``ngram.embed_fwd_drop``.
 
 A call runs on its tensors' device, on that device's current stream, whatever
 device is current in the calling thread."""
 from __future__ import annotations
+
+import ctypes
+import os
 
 import torch
 
@@ -11,6 +14,19 @@ import torch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def library(path: str, signatures: dict) -> ctypes.CDLL:
+    """The library at `path` with {name: (argument types, result type)} set."""
+    if not os.path.exists(path):
+        raise RuntimeError(f"libngram is not built ({path} missing): run "
+                           "`python -m sparse_hashed_gram_amd.build`")
+    L = ctypes.CDLL(path)
+    for name, (args, res) in signatures.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = res
+    return L
 
 
 def ptr(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None) -> int:

@@ -46,23 +46,14 @@ _lib = None
 def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
-        if not os.path.exists(_LIB_PATH):
-            raise RuntimeError(f"libngram is not built ({_LIB_PATH} missing): run "
-                               "`python -m sparse_hashed_gram_amd.build`")
-        L = ctypes.CDLL(_LIB_PATH)
         vp, i64, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
         sp = ctypes.POINTER(DropSpec)
-        sig = {
+        _lib = _marshal.library(_LIB_PATH, {
             "drop_abi_version": ([], i),
             "drop_status_string": ([i], ctypes.c_char_p),
             "drop_fwd": ([sp, vp, i, vp, vp, i, i64, i64, vp], i),
             "drop_bwd": ([sp, vp, i, vp, i, i64, i64, vp], i),
-        }
-        for name, (args, res) in sig.items():
-            f = getattr(L, name)
-            f.argtypes = args
-            f.restype = res
-        _lib = L
+        })
     return _lib
 
 

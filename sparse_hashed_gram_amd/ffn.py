@@ -80,25 +80,16 @@ _lib = None
 def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
-        if not os.path.exists(_LIB_PATH):
-            raise RuntimeError(f"libngram is not built ({_LIB_PATH} missing): run "
-                               "`python -m sparse_hashed_gram_amd.build`")
-        L = ctypes.CDLL(_LIB_PATH)
         vp, i64, i, u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
         cp, sp = ctypes.POINTER(FfnConfig), ctypes.POINTER(DropSpec)
-        sig = {
+        _lib = _marshal.library(_LIB_PATH, {
             "ffn_abi_version": ([], i),
             "ffn_status_string": ([i], ctypes.c_char_p),
             "ffn_config_check": ([cp], i),
             "ffn_workspace_bytes": ([cp, i, vp], i),
             "ffn_fwd": ([cp, vp, u64, vp, vp, vp, vp, vp, sp, i64, vp, vp], i),
             "ffn_bwd": ([cp, vp, u64, vp, vp, vp, vp, vp, sp, i64, vp, vp, vp, vp, vp], i),
-        }
-        for name, (args, res) in sig.items():
-            f = getattr(L, name)
-            f.argtypes = args
-            f.restype = res
-        _lib = L
+        })
     return _lib
 
 

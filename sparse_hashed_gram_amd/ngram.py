@@ -118,13 +118,9 @@ _lib = None
 def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
-        if not os.path.exists(_LIB_PATH):
-            raise RuntimeError(f"libngram is not built ({_LIB_PATH} missing): run "
-                               "`python -m sparse_hashed_gram_amd.build`")
-        L = ctypes.CDLL(_LIB_PATH)
         vp, i32, i64, u64p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
         cp = ctypes.POINTER(NgramConfig)
-        sig = {
+        _lib = _marshal.library(_LIB_PATH, {
             "ngram_abi_version": ([], ctypes.c_int),
             "ngram_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "ngram_config_check": ([cp], ctypes.c_int),
@@ -149,12 +145,7 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_float, ctypes.c_float, vp, vp], ctypes.c_int),
             "ngram_device_status": ([cp, vp, vp, ctypes.c_int, vp], ctypes.c_int),
             "ngram_profile_events": ([ctypes.c_int, vp, vp], ctypes.c_int),
-        }
-        for name, (args, res) in sig.items():
-            f = getattr(L, name)
-            f.argtypes = args
-            f.restype = res
-        _lib = L
+        })
     return _lib
 
 

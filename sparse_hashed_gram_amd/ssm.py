@@ -10,6 +10,8 @@ import os
 
 import torch
 
+from . import _marshal
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libngram.so")
 
 DIM = 768
@@ -63,13 +65,9 @@ _lib = None
 def lib() -> ctypes.CDLL:
     global _lib
     if _lib is None:
-        if not os.path.exists(_LIB_PATH):
-            raise RuntimeError(f"libngram is not built ({_LIB_PATH} missing): run "
-                               "`python -m sparse_hashed_gram_amd.build`")
-        L = ctypes.CDLL(_LIB_PATH)
         vp, i64 = ctypes.c_void_p, ctypes.c_int64
         cp = ctypes.POINTER(SsmConfig)
-        sig = {
+        _lib = _marshal.library(_LIB_PATH, {
             "ssm_abi_version": ([], ctypes.c_int),
             "ssm_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "ssm_workspace_bytes": ([cp, vp], ctypes.c_int),
@@ -79,12 +77,7 @@ def lib() -> ctypes.CDLL:
             "ssm_loss_bwd": ([cp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp], ctypes.c_int),
             "ssm_device_status": ([cp, vp, vp, ctypes.c_int, vp], ctypes.c_int),
             "ssm_profile_events": ([ctypes.c_int, vp, vp], ctypes.c_int),
-        }
-        for name, (args, res) in sig.items():
-            f = getattr(L, name)
-            f.argtypes = args
-            f.restype = res
-        _lib = L
+        })
     return _lib
 
 
