@@ -39,7 +39,7 @@ constexpr int kFewT = 64;   // most positions of wide_rows: one stage of the wei
 // are summed).  What T F, the number of values rounded, decides is how far the
 // error of one call's results (their norm) strays from that: up to 1.8 times the
 // own rounding's at T F = 128 - 424, 1.66 at 2,048, 1.56 at 4,096 - 8,192, 1.5 at
-// 16,384, 1.42 at 257,000 (120 calls of each size).  So this is a bound of about
+// 16,384, 1.42 at 257,000 (24 - 120 calls of each size).  So this is a bound of about
 // 1.5 on a call's error, not a promise about one element.  Every F of 128 or more
 // meets it by T F alone; narrower layers of more than 64 positions do not get it.
 // In a captured graph: forward of 1 x 2048 7.9 -> 8.5 us, 32 x 256 7.7 -> 8.4, 64 x 128
