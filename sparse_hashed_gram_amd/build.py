@@ -1,6 +1,8 @@
 """Builds libngram.so (HIP, gfx950) in-tree with hipcc: the n-gram table
 (include/ngram.h), the sampled-softmax loss (include/ssm.h), counter-based
-dropout (include/drop.h) and the gated feed-forward block (include/ffn.h).
+dropout (include/drop.h), the gated feed-forward block (include/ffn.h), the
+norms around a block (include/norm.h) and a gated linear recurrence
+(include/recur.h).
 
     python -m sparse_hashed_gram_amd.build
 
@@ -21,7 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libngram.so")
 SOURCES = ["ngram_abi.hip", "ngram_fwd.hip", "ngram_reduce.hip", "ngram_step.hip", "ngram_drop.hip", "ssm.hip",
-           "drop.hip", "ffn.hip"]
+           "drop.hip", "ffn.hip", "norm_abi.hip", "norm_fwd.hip", "norm_bwd.hip",
+           "recur.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
