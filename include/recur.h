@@ -27,7 +27,7 @@
  * Sequences: offsets (device, int32 [n + 1], ascending from >= 0 to <= T):
  * sequence k is rows offsets[k] .. offsets[k + 1] - 1; one without rows has hT =
  * h0 (or 0), dh0 = dhT (or 0).  Rows in front of the first and behind the last
- * sequence are neither read nor written.  offsets NULL: n has to be 1, and the
+ * sequence count for nothing and are left as they were in every output.  offsets NULL: n has to be 1, and the
  * sequence is all T rows.  Offsets that do not ascend give unspecified results,
  * but nothing outside the buffers is touched.  Nothing of one sequence reaches
  * another, NaN and infinities included; within a sequence a NaN stays.
@@ -62,7 +62,9 @@ extern "C" {
 #define RECUR_ECONFIG -3 /* the config is invalid                              */
 #define RECUR_ESIZE -4   /* T outside [0, max_tokens], n outside [0, 2^24] (1
                             without offsets), a distance between rows under D or
-                            over 2^31 - 1, or a workspace too small            */
+                            over 2^31 - 1, a workspace too small, or 2^23 and
+                            more pieces of 64 positions by 128 (D up to 64: 64)
+                            channels                                           */
 #define RECUR_EARG -5    /* an output that overlaps an operand or another output,
                             or an unknown pass                                 */
 #define RECUR_EHIP -6    /* the HIP runtime reported an error                  */
@@ -111,7 +113,7 @@ const char *recur_status_string(int status);
 int recur_config_check(const recur_config *cfg);
 
 /* Bytes of workspace that a pass of cfg needs (host output `bytes`); one of the
- * backward's size serves both.  About D max_tokens / 3 bytes. */
+ * backward's size serves both.  About D max_tokens / 5 bytes. */
 int recur_workspace_bytes(const recur_config *cfg, int pass, uint64_t *bytes);
 
 /* Bytes of `saved` for T positions: 4 D ceil(T / RECUR_CHUNK). */

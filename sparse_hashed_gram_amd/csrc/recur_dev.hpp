@@ -10,6 +10,11 @@
 
 namespace recur {
 
+constexpr int kChunk = RECUR_CHUNK;   // positions of a block
+constexpr int kWaves = 8;             // wavefronts of a block
+constexpr int kSteps = kChunk / kWaves;
+constexpr int kGroup = 32;            // chunks between two states that are passed on
+
 struct Args {
     const uint8_t *x, *r, *i, *dy;
     int64_t ldx, ldr, ldi;   // bytes
@@ -19,8 +24,13 @@ struct Args {
     int64_t lddx, lddr, lddi;   // bytes
     float *hT, *saved, *dlam, *dh0;
     int64_t T, n;
-    int D, accum;
+    int D, accum, chunks, columns;   // columns: blocks side by side
     float c;
+    // workspace
+    uint32_t *ticket;
+    uint64_t *sums;     // [chunks][D]: a chunk's (A, H)
+    uint64_t *states;   // [chunks / kGroup + 1][D]: the state in front of a group
+    float *part;        // [chunks][D]: the backward's sums for dlam
 };
 
 // s(v) and 1 - s(v), neither a difference of numbers near 1.
@@ -55,6 +65,11 @@ __device__ __forceinline__ float alone(float a, float b)
     return a * b;
 }
 
+// The value is computed where this stands.  Otherwise the compiler moves a product
+// down to the branch that uses it, and its factors stay in registers until then (256
+// registers and spills instead of 155 to 169 in the backward).
+__device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
+
 struct Gates {
     float a, m, g, g_rest, rho, rho_rest;
 };
@@ -72,22 +87,109 @@ __device__ __forceinline__ Gates gates(float r, float i, float k)
     return t;
 }
 
-template <int E>
-__device__ __forceinline__ float load1(const uint8_t *p)
+// V channels side by side as floats.  Rows start at any element: the access
+// claims no more than the elements' own alignment (global memory takes it).
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
+typedef float f32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+
+template <int E, int V>
+struct Raw;
+template <>
+struct Raw<2, 1> {
+    uint16_t w;
+};
+template <>
+struct Raw<2, 2> {
+    uint32_t w;
+};
+template <>
+struct Raw<4, 1> {
+    float w;
+};
+template <>
+struct Raw<4, 2> {
+    f32x2_a4 w;
+};
+
+template <int E, int V>
+__device__ __forceinline__ Raw<E, V> load(const uint8_t *p)
 {
-    if constexpr (E == 2)
-        return __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(p) << 16);
+    Raw<E, V> r;
+    if constexpr (E == 2 && V == 2)
+        r.w = *reinterpret_cast<const u32_a2 *>(p);
     else
-        return *reinterpret_cast<const float *>(p);
+        r.w = *reinterpret_cast<const decltype(r.w) *>(p);
+    return r;
 }
 
-template <int E>
-__device__ __forceinline__ void store1(uint8_t *p, float v)
+template <int E, int V>
+__device__ __forceinline__ void unpack(const Raw<E, V> &r, float (&v)[V])
 {
-    if constexpr (E == 2)
-        *reinterpret_cast<uint16_t *>(p) = (uint16_t)ngram::bf16_pack_rne(v, 0.0f);
+    if constexpr (E == 2 && V == 2) {
+        v[0] = ngram::bf16_lo(r.w);
+        v[1] = ngram::bf16_hi(r.w);
+    } else if constexpr (E == 2) {
+        v[0] = __uint_as_float((uint32_t)r.w << 16);
+    } else if constexpr (V == 2) {
+        v[0] = r.w[0];
+        v[1] = r.w[1];
+    } else {
+        v[0] = r.w;
+    }
+}
+
+template <int E, int V>
+__device__ __forceinline__ void store(uint8_t *p, const float (&v)[V])
+{
+    if constexpr (E == 2 && V == 2)
+        *reinterpret_cast<u32_a2 *>(p) = ngram::bf16_pack_rne(v[0], v[1]);
+    else if constexpr (E == 2)
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)ngram::bf16_pack_rne(v[0], 0.0f);
+    else if constexpr (V == 2)
+        *reinterpret_cast<f32x2_a4 *>(p) = f32x2_a4{v[0], v[1]};
     else
-        *reinterpret_cast<float *>(p) = v;
+        *reinterpret_cast<float *>(p) = v[0];
+}
+
+// A stretch of positions takes the state h in front of it to A h + H, or, where a
+// sequence begins in it, to H: A is -1 then (a product of a's is never negative),
+// so that an infinity or NaN of the sequence before does not come through a 0 A.
+struct Span1 {
+    float A, H;
+};
+
+__device__ __forceinline__ float through(const Span1 &s, float h) { return s.A < 0.0f ? s.H : __builtin_fmaf(s.A, h, s.H); }
+
+// First p, then q.
+__device__ __forceinline__ Span1 join(const Span1 &p, const Span1 &q)
+{
+    Span1 r;
+    r.A = q.A < 0.0f || p.A < 0.0f ? -1.0f : p.A * q.A;
+    r.H = through(q, p.H);
+    return r;
+}
+
+// Words of the workspace that one block writes and others wait for: a value that
+// says by itself that it is there (kNone is not), so no other memory has to be
+// ordered with it.
+constexpr uint64_t kNone = ~0ull;
+
+__device__ __forceinline__ uint64_t word(const Span1 &s)
+{
+    const uint32_t A = s.A != s.A ? 0x7FC00000u : __float_as_uint(s.A);
+    return (uint64_t)__float_as_uint(s.H) << 32 | A;
+}
+__device__ __forceinline__ Span1 span(uint64_t w)
+{
+    return Span1{__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+__device__ __forceinline__ void publish(uint64_t *p, uint64_t w)
+{
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 }   // namespace recur
