@@ -135,7 +135,7 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
  * state row slots[k] (slots NULL: row k, and `states` >= n), fp32 [states][D], one
  * position on, in place, and y gets its new values.  A row whose slot is negative
  * or not below `states` is unused: its y is 0.  Rows of the same slot are that
- * state's next positions, in the rows' order.  n in [0, 2^20]; T and max_tokens
+ * state's next positions, in the rows' order.  n in [0, 2^16]; T and max_tokens
  * do not count here. */
 int recur_step(const recur_config *cfg, const recur_inputs *in, const float *lam, float *state, int64_t states,
                const int32_t *slots, int64_t n, void *y, void *stream);

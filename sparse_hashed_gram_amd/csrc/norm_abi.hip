@@ -53,14 +53,14 @@ __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
     const int first = what == 0 ? kSumPreW : what == 1 ? kSumPost1 : kSumScale;
     const int second = what == 0 ? (a.db ? kSumPreB : -1)
                      : what == 1 ? (a.dpost_b || (a.dgate && a.p.post_b) ? kSumPost0 : -1) : -1;
-    float x = 0.0f, y = 0.0f;
+    float x = 0.0f, y = 0.0f;   // without a second sum, y is the first again and not looked at
     if (j < a.D) {
-        const float *p = a.part + (int64_t)g * kSums * ld + j;
-#pragma unroll 4
-        for (int i = g; i < a.parts; i += 16, p += (int64_t)16 * kSums * ld) {
-            x += p[first * ld];
-            if (second >= 0)
-                y += p[second * ld];
+        const float *p = a.part + (int64_t)g * kSums * ld + j + first * ld;
+        const int apart = second >= 0 ? (second - first) * ld : 0;
+#pragma unroll 16
+        for (int i = g; i < a.parts; i += 16, p += 16 * kSums * ld) {
+            x += p[0];
+            y += p[apart];
         }
     }
     lds[0][g][c] = x;

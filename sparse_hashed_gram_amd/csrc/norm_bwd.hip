@@ -7,10 +7,13 @@
 namespace rownorm {
 namespace {
 
+// q: what turns E into the gradient of the normalised B: gate (not a token's) times post_w
+enum { kW, kQ, kScale, kPostW, kPostB, kVectors };
+
 // xh and d -> the gradient in front of the norm over rho: d - [layer] mean(d) - xh mean(d xh).
 template <int W, int P>
-__device__ __forceinline__ void unnormalise(const float (&xh)[P][4], float (&d)[P][4], const int (&n)[P], int layer,
-                                            float inv_d, RowSum<W> &sum)
+__device__ __forceinline__ void unnormalise(const float (&xh)[P][4], float (&d)[P][4], int layer, float inv_d,
+                                            RowSum<W> &sum)
 {
     float c1 = 0.0f, c0 = 0.0f;
 #pragma unroll
@@ -35,144 +38,223 @@ __device__ __forceinline__ void unnormalise(const float (&xh)[P][4], float (&d)[
             d[p][k] = __builtin_fmaf(-xh[p][k], c1, d[p][k] - c0);
 }
 
-// A block's sums of a column: those of its rows' wavefronts, then to its part.
+// A block's sums of a column: those of its rows, then to its part.
 template <int W, int P>
-__device__ __forceinline__ void put(float (&v)[P][4], const int (&e)[P], int D, float *to, float (*lds)[P * 256])
+__device__ __forceinline__ void put(float (&v)[P][4], const Place<W> &me, int D, float *to,
+                                    float (*lds)[P * 256 * W])
 {
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    if constexpr (W == 1) {
+    if constexpr (kRows<W> > 1) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            *reinterpret_cast<float4 *>(&lds[wave][(p * 64 + lane) * 4]) = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+            *reinterpret_cast<float4 *>(&lds[me.row][(p * 64 * W + me.lane) * 4]) =
+                make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
         __syncthreads();
-        for (int j = threadIdx.x; j < D; j += kThreads<W>)
-            to[j] = (lds[0][j] + lds[1][j]) + (lds[2][j] + lds[3][j]);
+        for (int j = threadIdx.x; j < D; j += kThreads) {
+            float s = lds[0][j];
+#pragma unroll
+            for (int i = 1; i < kRows<W>; ++i)
+                s += lds[i][j];
+            to[j] = s;
+        }
         __syncthreads();
     } else {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            if (e[p] < D)   // parts are padded to whole pieces
-                *reinterpret_cast<float4 *>(to + e[p]) = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+        for (int p = 0; p < P; ++p) {
+            const int e = (p * 64 * W + me.lane) * 4;
+            if (e < D)   // parts are padded to whole pieces
+                *reinterpret_cast<float4 *>(to + e) = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
+        }
     }
 }
 
-template <int XE, int RE, int W, int P, bool JOIN, bool EXTRA>
-__global__ __launch_bounds__(kThreads<W>) void bwd_kernel(Args a)
+template <int XE, int RE, int P, bool FULL, bool JOIN, bool EXTRA>
+struct Row {
+    Piece<RE> r1[P], d1[P], r[P];
+    Piece<XE> dx[P], b[P], g[P];
+
+
+    __device__ __forceinline__ void load(const Args &a, int64_t row, const int (&e)[P], const int (&n)[P])
+    {
+        const int64_t at = min(row, a.T - 1) * a.D;
+        if (a.pre) {
+            load_row<RE, P, FULL>(a.R1in + at * RE, e, n, r1);
+            load_row<XE, P, FULL>(a.dX + at * XE, e, n, dx);
+        }
+        if constexpr (JOIN) {
+            load_row<XE, P, FULL>(a.B + at * XE, e, n, b);
+            if (a.G)
+                load_row<XE, P, FULL>(a.G + at * XE, e, n, g);
+        }
+        if (a.dR1)
+            load_row<RE, P, FULL>(a.dR1 + at * RE, e, n, d1);
+        else
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                d1[p].w = 0;
+        if constexpr (JOIN && EXTRA)
+            if (a.R)
+                load_row<RE, P, FULL>(a.R + at * RE, e, n, r);
+    }
+};
+
+template <int XE, int RE, int W, int P, bool FULL, bool JOIN, bool EXTRA>
+__global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
 {
-    __shared__ float2 red[2][W];
-    __shared__ float lds[W == 1 ? 4 : 1][P * 256];
-    RowSum<W> sum{red};
-    const int lane = W == 1 ? threadIdx.x % 64 : threadIdx.x;
+    constexpr int N = JOIN ? kVectors : 1;
+    __shared__ float2 red[2][8];
+    __shared__ float params[W == 1 ? N : 1][P * 256];
+    __shared__ float lds[kRows<W> > 1 ? kRows<W> : 1][P * 256 * W];
+    const Place<W> me;
+    const int lane = me.lane;
+    RowSum<W> sum{red, me.row};
+    ParamRows<W, P, N> par;
+    par.lds = params;
     int e[P], n[P];
-    // q: what turns E into the gradient of the normalised B: gate (not a token's) times post_w
-    float w[P][4], q[P][4], pw[P][4], pb[P][4], s[P][4];
     float sum_pre[P][4] = {}, sum_post[P][4] = {}, sum_preb[P][4] = {}, sum_post0[P][4] = {}, sum_s[P][4] = {};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         e[p] = (p * 64 * W + lane) * 4;
         n[p] = max(0, min(4, a.D - e[p]));
-        load_param(a.p.w, a.p.f32, 0, e[p], n[p], 1.0f, w[p]);
-        if constexpr (JOIN) {
-            load_param(a.p.post_w, a.p.f32, 0, e[p], n[p], 1.0f, pw[p]);
-            load_param(a.p.post_b, a.p.f32, 0, e[p], n[p], 0.0f, pb[p]);
-            load_param(a.G ? nullptr : a.p.gate, a.p.f32, a.p.gate_one, e[p], n[p], 1.0f, q[p]);
-            load_param(a.p.scale, a.p.f32, a.p.scale_one, e[p], n[p], 1.0f, s[p]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                q[p][k] *= pw[p][k];
-        }
     }
     const int64_t step = (int64_t)gridDim.x * kRows<W>;
-    for (int64_t row = (int64_t)blockIdx.x * kRows<W> + (W == 1 ? threadIdx.x / 64 : 0); row < a.T; row += step) {
+    int64_t row = (int64_t)blockIdx.x * kRows<W> + me.row, first = (int64_t)blockIdx.x * kRows<W>;
+    Row<XE, RE, P, FULL, JOIN, EXTRA> next;
+    next.load(a, row, e, n);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (W == 1 && me.row != i)   // a wavefront a vector
+            continue;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            float v[4];
+            if (i == kW) {
+                load_param(a.p.w, a.p.f32, 0, e[p], n[p], 1.0f, v);
+            } else if (i == kScale) {
+                load_param(a.p.scale, a.p.f32, a.p.scale_one, e[p], n[p], 1.0f, v);
+            } else if (i == kPostB) {
+                load_param(a.p.post_b, a.p.f32, 0, e[p], n[p], 0.0f, v);
+            } else {
+                load_param(a.p.post_w, a.p.f32, 0, e[p], n[p], 1.0f, v);
+                if (i == kQ) {
+                    float g[4];
+                    load_param(a.G ? nullptr : a.p.gate, a.p.f32, a.p.gate_one, e[p], n[p], 1.0f, g);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] *= g[k];
+                }
+            }
+            par.put(i, p, lane, v);
+        }
+    }
+    if constexpr (W == 1)
+        __syncthreads();
+    // every wavefront of the block takes as many turns: one without a row takes the last
+    // again, stores nothing and adds zeros
+    for (; first < a.T; first += step, row += step) {
+        const bool there = row < a.T;
+        if (W == 1 && !there)
+            break;
+        const Row<XE, RE, P, FULL, JOIN, EXTRA> cur = next;
+        next.load(a, row + step, e, n);
         const int64_t at = row * a.D;
         float d[P][4];   // E
         if (a.pre) {
-            float x[P][4], r[P][4];
+            float x[P][4];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                load4<RE>(a.R1in + (at + e[p]) * RE, n[p], x[p]);
-                load4<XE>(a.dX + (at + e[p]) * XE, n[p], d[p]);
+                unpack<RE>(cur.r1[p], x[p]);
+                unpack<XE>(cur.dx[p], d[p]);
+                if (W > 1 && !there)
+                    d[p][0] = d[p][1] = d[p][2] = d[p][3] = 0.0f;
             }
+            const float rho = normalise<W, P, FULL>(x, n, a.layer, a.inv_d, a.eps, sum);
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (a.dR1)
-                    load4<RE>(a.dR1 + (at + e[p]) * RE, n[p], r[p]);
-                else
-                    r[p][0] = r[p][1] = r[p][2] = r[p][3] = 0.0f;
-            }
-            const float rho = normalise<W, P>(x, n, a.layer, a.inv_d, a.eps, sum);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
+                float w[4];
+                par.get(kW, p, lane, w);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     sum_pre[p][k] = __builtin_fmaf(d[p][k], x[p][k], sum_pre[p][k]);
                     if constexpr (EXTRA)
                         sum_preb[p][k] += d[p][k];
-                    d[p][k] *= w[p][k];
+                    d[p][k] *= w[k];
                 }
-            unnormalise<W, P>(x, d, n, a.layer, a.inv_d, sum);
+            }
+            unnormalise<W, P>(x, d, a.layer, a.inv_d, sum);
 #pragma unroll
-            for (int p = 0; p < P; ++p)
+            for (int p = 0; p < P; ++p) {
+                float r[4];
+                unpack<RE>(cur.d1[p], r);
+                if (W > 1 && !there)
+                    r[0] = r[1] = r[2] = r[3] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    d[p][k] = k < n[p] ? __builtin_fmaf(rho, d[p][k], r[p][k]) : 0.0f;
+                    d[p][k] = FULL || k < n[p] ? __builtin_fmaf(rho, d[p][k], r[k]) : 0.0f;
+            }
         } else {
 #pragma unroll
-            for (int p = 0; p < P; ++p)
-                load4<RE>(a.dR1 + (at + e[p]) * RE, n[p], d[p]);
+            for (int p = 0; p < P; ++p) {
+                unpack<RE>(cur.d1[p], d[p]);
+                if (W > 1 && !there)
+                    d[p][0] = d[p][1] = d[p][2] = d[p][3] = 0.0f;
+            }
         }
         if constexpr (!JOIN) {
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                store4<RE>(a.dR + (at + e[p]) * RE, n[p], d[p]);
+                if (there)
+                    store4<RE, FULL>(a.dR + at * RE + (uint32_t)(e[p] * RE), n[p], d[p]);
         } else {
-            float v[P][4], t[P][4];
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                load4<XE>(a.B + (at + e[p]) * XE, n[p], v[p]);
-            if (a.G) {
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    load4<XE>(a.G + (at + e[p]) * XE, n[p], t[p]);
-            }
+            float v[P][4];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 float o[4];
                 if constexpr (EXTRA) {
                     if (a.R) {
-                        load4<RE>(a.R + (at + e[p]) * RE, n[p], o);
+                        unpack<RE>(cur.r[p], o);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             sum_s[p][k] = __builtin_fmaf(d[p][k], o[k], sum_s[p][k]);
                     }
                 }
+                par.get(kScale, p, lane, o);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    o[k] = d[p][k] * s[p][k];
-                store4<RE>(a.dR + (at + e[p]) * RE, n[p], o);
+                    o[k] *= d[p][k];
+                if (there)
+                    store4<RE, FULL>(a.dR + at * RE + (uint32_t)(e[p] * RE), n[p], o);
+                unpack<XE>(cur.b[p], v[p]);
             }
-            const float rho = a.post ? normalise<W, P>(v, n, a.layer, a.inv_d, a.eps, sum) : 1.0f;
+            const float rho = a.post ? normalise<W, P, FULL>(v, n, a.layer, a.inv_d, a.eps, sum) : 1.0f;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                float dg[4];
+                if (a.G) {
+                    float g[4], dg[4], pw[4], pb[4];
+                    unpack<XE>(cur.g[p], g);
+                    par.get(kPostW, p, lane, pw);
+                    par.get(kPostB, p, lane, pb);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float slope;
+                        g[k] = sigmoid(g[k], slope);
+                        dg[k] = d[p][k] * __builtin_fmaf(v[p][k], pw[k], pb[k]) * slope;
+                        d[p][k] *= g[k];
+                    }
+                    if (a.dG && there)
+                        store4<XE, FULL>(a.dG + at * XE + (uint32_t)(e[p] * XE), n[p], dg);
+                }
+                float q[4];
+                par.get(kQ, p, lane, q);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (a.G) {
-                        float slope;
-                        const float gk = sigmoid(t[p][k], slope);
-                        dg[k] = d[p][k] * __builtin_fmaf(v[p][k], pw[p][k], pb[p][k]) * slope;
-                        d[p][k] *= gk;
-                    }
                     sum_post[p][k] = __builtin_fmaf(d[p][k], v[p][k], sum_post[p][k]);
                     if constexpr (EXTRA)
                         sum_post0[p][k] += d[p][k];
-                    d[p][k] *= q[p][k];
+                    d[p][k] *= q[k];
                 }
-                if (a.G && a.dG)
-                    store4<XE>(a.dG + (at + e[p]) * XE, n[p], dg);
             }
             if (a.post) {
-                unnormalise<W, P>(v, d, n, a.layer, a.inv_d, sum);
+                unnormalise<W, P>(v, d, a.layer, a.inv_d, sum);
 #pragma unroll
                 for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -181,39 +263,39 @@ __global__ __launch_bounds__(kThreads<W>) void bwd_kernel(Args a)
             }
 #pragma unroll
             for (int p = 0; p < P; ++p)
-                store4<XE>(a.dB + (at + e[p]) * XE, n[p], d[p]);
+                if (there)
+                    store4<XE, FULL>(a.dB + at * XE + (uint32_t)(e[p] * XE), n[p], d[p]);
         }
     }
     const int ld = (a.D + 3) / 4 * 4;
     float *to = a.part + (int64_t)blockIdx.x * kSums * ld;
-    put<W, P>(sum_pre, e, a.D, to + kSumPreW * ld, lds);
+    put<W, P>(sum_pre, me, a.D, to + kSumPreW * ld, lds);
     if constexpr (JOIN)
-        put<W, P>(sum_post, e, a.D, to + kSumPost1 * ld, lds);
+        put<W, P>(sum_post, me, a.D, to + kSumPost1 * ld, lds);
     if constexpr (EXTRA) {
-        put<W, P>(sum_preb, e, a.D, to + kSumPreB * ld, lds);
+        put<W, P>(sum_preb, me, a.D, to + kSumPreB * ld, lds);
         if constexpr (JOIN) {
-            put<W, P>(sum_post0, e, a.D, to + kSumPost0 * ld, lds);
-            put<W, P>(sum_s, e, a.D, to + kSumScale * ld, lds);
+            put<W, P>(sum_post0, me, a.D, to + kSumPost0 * ld, lds);
+            put<W, P>(sum_s, me, a.D, to + kSumScale * ld, lds);
         }
     }
+}
+
+template <int XE, int RE, int W, int P, bool FULL>
+int launch_as(const Args &a, bool extra, hipStream_t s)
+{
+    // as many blocks as run at once: one a compute unit with the join's registers, two without
+    const int grid = (int)std::min<int64_t>((a.T + kRows<W> - 1) / kRows<W>, a.dB ? 256 : kMaxBlocks);
+    auto k = a.dB ? (extra ? bwd_kernel<XE, RE, W, P, FULL, true, true> : bwd_kernel<XE, RE, W, P, FULL, true, false>)
+                  : (extra ? bwd_kernel<XE, RE, W, P, FULL, false, true> : bwd_kernel<XE, RE, W, P, FULL, false, false>);
+    k<<<grid, kThreads, 0, s>>>(a);
+    return grid;
 }
 
 template <int XE, int RE, int W, int P>
 int launch(const Args &a, bool extra, hipStream_t s)
 {
-    const int grid = (int)std::min<int64_t>((a.T + kRows<W> - 1) / kRows<W>, kMaxBlocks);
-    if (a.dB) {
-        if (extra)
-            bwd_kernel<XE, RE, W, P, true, true><<<grid, kThreads<W>, 0, s>>>(a);
-        else
-            bwd_kernel<XE, RE, W, P, true, false><<<grid, kThreads<W>, 0, s>>>(a);
-    } else {
-        if (extra)
-            bwd_kernel<XE, RE, W, P, false, true><<<grid, kThreads<W>, 0, s>>>(a);
-        else
-            bwd_kernel<XE, RE, W, P, false, false><<<grid, kThreads<W>, 0, s>>>(a);
-    }
-    return grid;
+    return a.D == 256 * W * P ? launch_as<XE, RE, W, P, true>(a, extra, s) : launch_as<XE, RE, W, P, false>(a, extra, s);
 }
 
 template <int XE, int RE>
@@ -221,13 +303,15 @@ int by_width(const Args &a, bool extra, hipStream_t s)
 {
     if (a.D <= 256)
         return launch<XE, RE, 1, 1>(a, extra, s);
+    if (a.D <= 512)
+        return launch<XE, RE, 1, 2>(a, extra, s);
     if (a.D <= 768)
         return launch<XE, RE, 1, 3>(a, extra, s);
     if (a.D <= 1024)
-        return launch<XE, RE, 1, 4>(a, extra, s);
+        return launch<XE, RE, 2, 2>(a, extra, s);
     if (a.D <= 2048)
-        return launch<XE, RE, 2, 4>(a, extra, s);
-    return launch<XE, RE, 4, 4>(a, extra, s);
+        return launch<XE, RE, 4, 2>(a, extra, s);
+    return launch<XE, RE, 8, 2>(a, extra, s);
 }
 
 }   // namespace

@@ -118,6 +118,7 @@ template <int V>
 struct Shared {
     Span1 waves[kWaves][V][64];   // each wavefront's stretch
     Span1 before[kWaves][V][64];  // stretches of the chunks before, kGroup / kWaves a wavefront
+    Span1 all[V][64];             // the chunk
     float state[V][64];           // the state in front of the group of chunks
     Marks marks;
 };
@@ -128,86 +129,116 @@ struct Shared {
 //
 // Every chunk says what it does to a state (sums) as soon as it knows it, without
 // waiting for anyone; the last chunk of a group of kGroup says what state it leaves
-// (states).  A chunk takes the state in front of its group and goes through the
-// group's earlier chunks, always in the same order, so that results do not depend
-// on who came first.  A wait ends: who is waited for has begun to run (place), and
-// waits itself only for chunks in front of it; should one never answer, the values
-// become NaN after a bounded number of polls.
+// (states), so only those form a chain, and one of them hands on as soon as the one
+// before has.  A chunk takes the state in front of its group through the group's
+// earlier chunks, always in the same order: results do not depend on who came
+// first.  A wait ends: who is waited for has begun to run (place), and waits itself
+// only for chunks in front of it; should one never answer, the values become NaN
+// after a bounded number of polls.
+constexpr int kPolls = 1 << 20;
+
+__device__ __forceinline__ uint64_t wait_for(const uint64_t *p, uint64_t w)
+{
+    for (int polls = 0; polls < kPolls && __any(w == kNone); ++polls) {
+        __builtin_amdgcn_s_sleep(4);
+        if (w == kNone)
+            w = peek(p);
+    }
+    return w;
+}
+
 template <int V>
-__device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int index, int wave, int order, int lane,
-                                             int j, const Span1 (&own)[V], float (&h)[V])
+__device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int index, int column, int wave, int order,
+                                             int lane, const Span1 (&own)[V], float (&h)[V])
 {
 #pragma unroll
     for (int v = 0; v < V; ++v)
         sh.waves[order][v][lane] = own[v];
     __syncthreads();
-    if (a.chunks > 1) {
-        Span1 all[V];
-        if (wave == 0) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                all[v] = sh.waves[0][v][lane];
-#pragma unroll
-                for (int w = 1; w < kWaves; ++w)
-                    all[v] = join(all[v], sh.waves[w][v][lane]);
-                publish(&a.sums[(int64_t)index * a.D + j + v], word(all[v]));
-            }
-        }
-        const int group = index / kGroup, place = index % kGroup, per = kGroup / kWaves;
-        uint64_t w[per][V], s[V];
-        const bool first = wave == kWaves - 1 && group > 0;
-        for (int polls = 0; polls < (1 << 20); ++polls) {
-            bool there = true;
-#pragma unroll
-            for (int i = 0; i < per; ++i)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    w[i][v] = 0;
-                    if (wave * per + i < place)
-                        w[i][v] = peek(&a.sums[((int64_t)group * kGroup + wave * per + i) * a.D + j + v]);
-                }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = 0;
-                if (first)
-                    s[v] = peek(&a.states[(int64_t)group * a.D + j + v]);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                there = there && s[v] != kNone;
-#pragma unroll
-                for (int i = 0; i < per; ++i)
-                    there = there && w[i][v] != kNone;
-            }
-            if (__all(there))
-                break;
-            __builtin_amdgcn_s_sleep(1);
-        }
+    for (int v = 0; v < V; ++v)
+        h[v] = 0.0f;
+    if (a.chunks <= 1)
+        return;
+    constexpr int per = kGroup / kWaves;
+    const int group = index / kGroup, place = index % kGroup;
+    const int64_t step = (int64_t)a.columns * V * 64;   // words of a chunk
+    const int at = column * V * 64 + lane;
+    if (wave == kWaves - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            Span1 p{1.0f, 0.0f};
+            Span1 all = sh.waves[0][v][lane];
 #pragma unroll
-            for (int i = 0; i < per; ++i)
-                if (wave * per + i < place)
-                    p = join(p, span(w[i][v]));
-            sh.before[wave][v][lane] = p;
-            if (wave == kWaves - 1)
-                sh.state[v][lane] = group > 0 ? span(s[v]).H : 0.0f;
+            for (int w = 1; w < kWaves; ++w)
+                all = join(all, sh.waves[w][v][lane]);
+            publish(&a.sums[index * step + at + v * 64], word(all));
+            sh.all[v][lane] = all;
+        }
+    }
+    if (place > 0) {
+        const uint64_t *p = a.sums + ((int64_t)group * kGroup + wave * per) * step + at;
+        const int mine = min(per, place - wave * per);   // chunks before that this wavefront looks at
+        uint64_t w[per][V];
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+            if (i < mine)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    w[i][v] = peek(p + i * step + v * 64);
+        Span1 s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            s[v] = Span1{1.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+            if (i < mine)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    s[v] = join(s[v], span(wait_for(p + i * step + v * 64, w[i][v])));
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            sh.before[wave][v][lane] = s[v];
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            s[v] = sh.before[0][v][lane];
+        for (int i = 1; i * per < place; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s[v] = join(s[v], sh.before[i][v][lane]);
+        if (group > 0 || place == kGroup - 1) {
+            if (wave == kWaves - 1) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    h[v] = group > 0 ? span(wait_for(a.states + group * step + at + v * 64, kNone)).H : 0.0f;
+                if (place == kGroup - 1 && index + 1 < a.chunks) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        publish(a.states + (group + 1) * step + at + v * 64,
+                                word(Span1{1.0f, through(sh.all[v][lane], through(s[v], h[v]))}));
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    sh.state[v][lane] = h[v];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = sh.state[v][lane];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            h[v] = through(s[v], h[v]);
+    } else if (group > 0) {
+        if (wave == kWaves - 1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                sh.state[v][lane] = span(wait_for(a.states + group * step + at + v * 64, kNone)).H;
         }
         __syncthreads();
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            h[v] = sh.state[v][lane];
-#pragma unroll
-            for (int i = 0; i < kWaves; ++i)
-                h[v] = through(sh.before[i][v][lane], h[v]);
-            if (wave == 0 && place == kGroup - 1 && index + 1 < a.chunks)
-                publish(&a.states[(int64_t)(group + 1) * a.D + j + v], word(Span1{1.0f, through(all[v], h[v])}));
-        }
-    } else {
-#pragma unroll
         for (int v = 0; v < V; ++v)
-            h[v] = 0.0f;
+            h[v] = sh.state[v][lane];
     }
 }
 
@@ -217,7 +248,7 @@ __global__ __launch_bounds__(256) void clear_kernel(Args a, const float *in, flo
 {
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
     if (a.chunks > 1) {
-        const int64_t words = (int64_t)(a.chunks + a.chunks / kGroup + 1) * a.D;   // sums, then states
+        const int64_t words = a.words;   // sums, then states
         for (int64_t k = first; k < words; k += step)
             a.sums[k] = kNone;
         if (first == 0)
@@ -234,6 +265,45 @@ __global__ __launch_bounds__(256) void clear_kernel(Args a, const float *in, flo
     }
 }
 
+// kSteps rows from t on; rows behind the last are the last again.
+template <int E, int V>
+__device__ __forceinline__ void load_rows(const uint8_t *p, int64_t ld, int64_t t, int64_t T, uint32_t off,
+                                          Raw<E, V> (&v)[kSteps])
+{
+    p += t * ld;
+    if (t + kSteps <= T) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            v[k] = load<E, V>(p + off);
+            p += ld;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            v[k] = load<E, V>(p + (min(t + k, T - 1) - t) * ld + off);
+    }
+}
+
+template <int E, int V, bool ALL>
+__device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kSteps], const Raw<E, V> (&r)[kSteps],
+                                          const Raw<E, V> (&i)[kSteps], const float (&rate)[V], float (&av)[kSteps][V],
+                                          float (&u)[kSteps][V])
+{
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        float xf[V], rf[V], gf[V];
+        unpack<E, V>(x[k], xf);
+        unpack<E, V>(r[k], rf);
+        unpack<E, V>(i[k], gf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float m;
+            decays<ALL>(rate[v] * sigmoid(rf[v]), av[k][v], m);
+            u[k][v] = m * sigmoid(gf[v]) * xf[v];
+        }
+    }
+}
+
 template <int E, int V>
 __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
 {
@@ -245,77 +315,72 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;   // behind a row's address, which is the same for all lanes
     const int64_t t0 = (int64_t)chunk * kChunk, t = t0 + wave * kSteps;
-    int64_t lo, hi;
-    rows_of_sequences(a, lo, hi);
-    if (t0 >= hi)
-        return;   // nor does any chunk behind it ask
     Raw<E, V> x[kSteps], r[kSteps], i[kSteps];
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        const int64_t row = min(t + k, a.T - 1);
-        r[k] = load<E, V>(a.r + row * a.ldr + off);
-        i[k] = load<E, V>(a.i + row * a.ldi + off);
-        x[k] = load<E, V>(a.x + row * a.ldx + off);
-    }
+    load_rows<E, V>(a.r, a.ldr, t, a.T, off, r);
+    load_rows<E, V>(a.i, a.ldi, t, a.T, off, i);
+    load_rows<E, V>(a.x, a.ldx, t, a.T, off, x);
     float rate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
         rate[v] = decay(a.lam[j + v], a.c);
+    int64_t lo, hi;
+    rows_of_sequences(a, lo, hi);
+    if (t0 >= hi)
+        return;   // nor does any chunk behind it ask
     if (a.offsets)
         find_marks(a, t0, &sh.marks);
     const Bits bits = bits_of(a, &sh.marks, t0, lo, hi, wave);
+    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << kSteps) - 1;
     float av[kSteps][V], u[kSteps][V];
+    bool all = true;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        float xf[V], rf[V], gf[V];
-        unpack<E, V>(x[k], xf);
-        unpack<E, V>(r[k], rf);
-        unpack<E, V>(i[k], gf);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Gates q = gates(rf[v], gf[v], rate[v]);
-            av[k][v] = q.a;
-            u[k][v] = q.m * q.g * xf[v];
-        }
-    }
+    for (int v = 0; v < V; ++v)
+        all = all && rate[v] > kSeries;
+    if (__all(all))
+        fwd_gates<E, V, true>(x, r, i, rate, av, u);
+    else
+        fwd_gates<E, V, false>(x, r, i, rate, av, u);
     Span1 own[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
         own[v] = Span1{1.0f, 0.0f};
+    if (plain) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        if (!(bits.inside >> k & 1)) {
+        for (int k = 0; k < kSteps; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                av[k][v] = 1.0f;
-                u[k][v] = 0.0f;
+                own[v].A *= av[k][v];
+                own[v].H = __builtin_fmaf(av[k][v], own[v].H, u[k][v]);
             }
-        }
-        if (bits.starts >> k & 1) {
-            if (a.h0) {
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const bool start = bits.starts >> k & 1, inside = bits.inside >> k & 1;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                av[k][v] = inside ? av[k][v] : 1.0f;
+                u[k][v] = inside ? u[k][v] : 0.0f;
+            }
+            if (start && a.h0) {
                 const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     u[k][v] = __builtin_fmaf(av[k][v], a.h0[s * a.D + j + v], u[k][v]);
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                own[v].H = u[k][v];
-        } else {
-#pragma unroll
             for (int v = 0; v < V; ++v) {
                 own[v].A *= av[k][v];
-                own[v].H = __builtin_fmaf(av[k][v], own[v].H, u[k][v]);
+                own[v].H = start ? u[k][v] : __builtin_fmaf(av[k][v], own[v].H, u[k][v]);
             }
         }
-    }
-    if (bits.starts) {
+        if (bits.starts) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            own[v].A = -1.0f;
+            for (int v = 0; v < V; ++v)
+                own[v].A = -1.0f;
+        }
     }
     float h[V];
-    state_before<V>(a, sh, chunk, wave, wave, lane, j, own, h);
+    state_before<V>(a, sh, chunk, column, wave, wave, lane, own, h);
     if (a.saved && wave == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -325,18 +390,81 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             h[v] = through(sh.waves[w][v][lane], h[v]);
+    uint8_t *y = a.y + t * a.D * E;
+    if (plain) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = bits.starts >> k & 1 ? u[k][v] : __builtin_fmaf(av[k][v], h[v], u[k][v]);
-        if (bits.inside >> k & 1)
-            store<E, V>(a.y + (t + k) * a.D * E + off, h);
-        if (a.hT && (bits.ends >> k & 1)) {
-            const int64_t s = a.offsets ? sh.marks.end_of[wave * kSteps + k] : 0;
+        for (int k = 0; k < kSteps; ++k) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                a.hT[s * a.D + j + v] = h[v];
+                h[v] = __builtin_fmaf(av[k][v], h[v], u[k][v]);
+            store<E, V>(y + off, h);
+            y += (int64_t)a.D * E;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = bits.starts >> k & 1 ? u[k][v] : __builtin_fmaf(av[k][v], h[v], u[k][v]);
+            if (bits.inside >> k & 1)
+                store<E, V>(y + off, h);
+            y += (int64_t)a.D * E;
+            if (a.hT && (bits.ends >> k & 1)) {
+                const int64_t s = a.offsets ? sh.marks.end_of[wave * kSteps + k] : 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    a.hT[s * a.D + j + v] = h[v];
+            }
+        }
+    }
+}
+
+// The sequence that begins or ends at the wavefront's position k.
+__device__ __forceinline__ int64_t sequence_of(const Args &a, const int (&of)[kChunk], int wave, int k)
+{
+    return a.offsets ? of[wave * kSteps + k] : 0;
+}
+
+// H = the sequence's row of h0 or dhT, 0 without them.
+template <int V>
+__device__ __forceinline__ void row_of(const float *p, int64_t sequence, int D, int j, Span1 (&to)[V])
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        to[v].H = p ? p[sequence * D + j + v] : 0.0f;
+}
+
+// A position's numbers that need no state: a, m g (dx / G), m g x (1 - g) (di / G), and
+// of dz / G the part beside a h_{t-1}: g x a^2 / m.
+template <int E, int V, bool ALL>
+__device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kSteps], const Raw<E, V> (&r)[kSteps],
+                                          const Raw<E, V> (&i)[kSteps], const float (&rate)[V], float (&av)[kSteps][V],
+                                          float (&c1)[kSteps][V], float (&c2)[kSteps][V],
+                                          float (&c3)[kSteps][V], float (&cr)[kSteps][V], float (&cl)[kSteps][V])
+{
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        float xf[V], rf[V], gf[V];
+        unpack<E, V>(x[k], xf);
+        unpack<E, V>(r[k], rf);
+        unpack<E, V>(i[k], gf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float rho, rho_rest, g, g_rest, m;
+            sigmoid(rf[v], rho, rho_rest);
+            sigmoid(gf[v], g, g_rest);
+            const float z = rate[v] * rho;
+            decays<ALL>(z, av[k][v], m);
+            c1[k][v] = m * g;
+            c2[k][v] = c1[k][v] * xf[v] * g_rest;
+            cl[k][v] = rho;
+            cr[k][v] = z * rho_rest;
+            c3[k][v] = m > 0.0f ? g * xf[v] * (av[k][v] * av[k][v] * __builtin_amdgcn_rcpf(m)) : 0.0f;
+            here(c1[k][v]);
+            here(c2[k][v]);
+            here(c3[k][v]);
+            here(cl[k][v]);
+            here(cr[k][v]);
         }
     }
 }
@@ -354,17 +482,13 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
     const int chunk = a.chunks - 1 - index;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int j = min((column * 64 + lane) * V, a.D - V);
-    const uint32_t off = (uint32_t)j * E;   // behind a row's address, which is the same for all lanes
+    const uint32_t off = (uint32_t)j * E;
     const int64_t t0 = (int64_t)chunk * kChunk, t = t0 + wave * kSteps;
     Raw<E, V> x[kSteps], r[kSteps], i[kSteps], d[kSteps];
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        const int64_t row = min(t + k, a.T - 1);
-        r[k] = load<E, V>(a.r + row * a.ldr + off);
-        i[k] = load<E, V>(a.i + row * a.ldi + off);
-        x[k] = load<E, V>(a.x + row * a.ldx + off);
-        d[k] = load<E, V>(a.dy + row * a.D * E + off);
-    }
+    load_rows<E, V>(a.r, a.ldr, t, a.T, off, r);
+    load_rows<E, V>(a.i, a.ldi, t, a.T, off, i);
+    load_rows<E, V>(a.x, a.ldx, t, a.T, off, x);
+    load_rows<E, V>(a.dy, (int64_t)a.D * E, t, a.T, off, d);
     float rate[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -376,53 +500,85 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
     if (a.offsets)
         find_marks(a, t0, &sh.marks);
     const Bits bits = bits_of(a, &sh.marks, t0, lo, hi, wave);
-    float av[kSteps][V], c1[kSteps][V], c2[kSteps][V], cr[kSteps][V], cl[kSteps][V], u[kSteps][V], c3[kSteps][V];
-    Span1 own[V];
+    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << kSteps) - 1;
+    float av[kSteps][V], c1[kSteps][V], c2[kSteps][V], c3[kSteps][V], cr[kSteps][V], cl[kSteps][V];
+    bool all = true;
 #pragma unroll
     for (int v = 0; v < V; ++v)
+        all = all && rate[v] > kSeries;
+    if (__all(all))
+        bwd_gates<E, V, true>(x, r, i, rate, av, c1, c2, c3, cr, cl);
+    else
+        bwd_gates<E, V, false>(x, r, i, rate, av, c1, c2, c3, cr, cl);
+    // forward: what the stretch does to a state; backward: what reaches it from behind
+    // goes to A in + H, with the same A
+    Span1 own[V], back[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
         own[v] = Span1{1.0f, 0.0f};
+        back[v].H = 0.0f;
+    }
+    if (plain) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-        float xf[V], rf[V], gf[V];
-        unpack<E, V>(x[k], xf);
-        unpack<E, V>(r[k], rf);
-        unpack<E, V>(i[k], gf);
-        const bool start = bits.starts >> k & 1, inside = bits.inside >> k & 1;
+        for (int k = 0; k < kSteps; ++k) {
+            float xf[V];
+            unpack<E, V>(x[k], xf);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Gates q = gates(rf[v], gf[v], rate[v]);
-            av[k][v] = inside ? q.a : 1.0f;
-            c1[k][v] = q.m * q.g;
-            u[k][v] = inside ? c1[k][v] * xf[v] : 0.0f;
-            c2[k][v] = u[k][v] * q.g_rest;
-            cl[k][v] = q.rho;
-            cr[k][v] = rate[v] * q.rho * q.rho_rest;
-            c3[k][v] = q.m > 0.0f ? q.g * xf[v] * (q.a * q.a * __builtin_amdgcn_rcpf(q.m)) : 0.0f;
+            for (int v = 0; v < V; ++v) {
+                own[v].A *= av[k][v];
+                own[v].H = __builtin_fmaf(av[k][v], own[v].H, c1[k][v] * xf[v]);
+            }
         }
-        if (start && a.h0) {
-            const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
+#pragma unroll
+        for (int k = kSteps - 1; k >= 0; --k) {
+            float df[V];
+            unpack<E, V>(d[k], df);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                u[k][v] = __builtin_fmaf(av[k][v], a.h0[s * a.D + j + v], u[k][v]);
+                back[v].H = av[k][v] * (df[v] + back[v].H);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            back[v].A = own[v].A;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if (!(bits.inside >> k & 1)) {
+                x[k].w = d[k].w = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    av[k][v] = 1.0f;
+            }
+            if (bits.starts >> k & 1)
+                row_of<V>(a.h0, sequence_of(a, sh.marks.start_of, wave, k), a.D, j, own);
+            float xf[V];
+            unpack<E, V>(x[k], xf);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                own[v].A *= av[k][v];
+                own[v].H = __builtin_fmaf(av[k][v], own[v].H, c1[k][v] * xf[v]);
+            }
+        }
+#pragma unroll
+        for (int k = kSteps - 1; k >= 0; --k) {
+            if (bits.ends >> k & 1)
+                row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of, wave, k), a.D, j, back);
+            float df[V];
+            unpack<E, V>(d[k], df);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                back[v].H = av[k][v] * (df[v] + back[v].H);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            own[v].A *= av[k][v];
-            own[v].H = start ? u[k][v] : __builtin_fmaf(av[k][v], own[v].H, u[k][v]);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            here(c1[k][v]);
-            here(c2[k][v]);
-            here(c3[k][v]);
-            here(cl[k][v]);
-            here(cr[k][v]);
+            back[v].A = bits.ends ? -1.0f : own[v].A;
+            own[v].A = bits.starts ? -1.0f : own[v].A;
         }
     }
     // h_{t-1}, and what it makes of the numbers above
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        sh.before[wave][v][lane] = Span1{bits.starts ? -1.0f : own[v].A, own[v].H};
+        sh.before[wave][v][lane] = own[v];
     __syncthreads();
     for (int w = 0; w < wave; ++w)
 #pragma unroll
@@ -430,49 +586,26 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
             h[v] = through(sh.before[w][v][lane], h[v]);
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-        const bool start = bits.starts >> k & 1;
-        if (start) {
-            const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
+        if (bits.starts >> k & 1) {
+            row_of<V>(a.h0, sequence_of(a, sh.marks.start_of, wave, k), a.D, j, own);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                h[v] = a.h0 ? a.h0[s * a.D + j + v] : 0.0f;
+                h[v] = own[v].H;
         }
+        float xf[V];
+        unpack<E, V>(x[k], xf);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float z = __builtin_fmaf(av[k][v], h[v], -c3[k][v]);   // dz / G
+            const float ah = av[k][v] * h[v], z = ah - c3[k][v];   // z: dz / G
             cr[k][v] *= z;
             cl[k][v] *= z;
             here(cr[k][v]);
             here(cl[k][v]);
-            h[v] = start ? u[k][v] : __builtin_fmaf(av[k][v], h[v], u[k][v]);
-        }
-    }
-    // the same backwards: what reaches the stretch from behind goes to A in + H
-    Span1 back[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        back[v] = Span1{bits.ends ? -1.0f : own[v].A, 0.0f};
-    float df[kSteps][V];
-#pragma unroll
-    for (int k = kSteps - 1; k >= 0; --k) {
-        unpack<E, V>(d[k], df[k]);
-        const bool end = bits.ends >> k & 1, inside = bits.inside >> k & 1;
-        if (end) {
-            const int64_t s = a.offsets ? sh.marks.end_of[wave * kSteps + k] : 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                back[v].H = a.dhT ? a.dhT[s * a.D + j + v] : 0.0f;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            df[k][v] = inside ? df[k][v] : 0.0f;
-            if (end)
-                df[k][v] += back[v].H;   // kept: the second walk then begins at 0 here
-            back[v].H = av[k][v] * (end ? df[k][v] : df[k][v] + back[v].H);
+            h[v] = __builtin_fmaf(c1[k][v], xf[v], ah);
         }
     }
     float in[V], acc[V];
-    state_before<V>(a, sh, index, wave, kWaves - 1 - wave, lane, j, back, in);
+    state_before<V>(a, sh, index, column, wave, kWaves - 1 - wave, lane, back, in);
     for (int w = 0; w < kWaves - 1 - wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -480,27 +613,38 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.0f;
+    uint8_t *px = a.dx + (t + kSteps - 1) * a.lddx, *pr = a.dr + (t + kSteps - 1) * a.lddr,
+            *pi = a.di + (t + kSteps - 1) * a.lddi;
 #pragma unroll
     for (int k = kSteps - 1; k >= 0; --k) {
-        const bool end = bits.ends >> k & 1;
-        float dx[V], di[V], dr[V];
+        if (bits.ends >> k & 1) {
+            row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of, wave, k), a.D, j, own);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                in[v] = own[v].H;
+        }
+        float df[V], dx[V], di[V], dr[V], dl[V];
+        unpack<E, V>(d[k], df);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float G = end ? df[k][v] : df[k][v] + in[v];
+            const float G = df[v] + in[v];
             in[v] = av[k][v] * G;
             dx[v] = G * c1[k][v];
             di[v] = G * c2[k][v];
             dr[v] = G * cr[k][v];
-            cl[k][v] *= G;
+            dl[v] = G * cl[k][v];
         }
         if (bits.inside >> k & 1) {
-            store<E, V>(a.dx + (t + k) * a.lddx + off, dx);
-            store<E, V>(a.di + (t + k) * a.lddi + off, di);
-            store<E, V>(a.dr + (t + k) * a.lddr + off, dr);
+            store<E, V>(px + off, dx);
+            store<E, V>(pi + off, di);
+            store<E, V>(pr + off, dr);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                acc[v] += cl[k][v];
+                acc[v] += dl[v];
         }
+        px -= a.lddx;
+        pr -= a.lddr;
+        pi -= a.lddi;
         if (a.dh0 && (bits.starts >> k & 1)) {
             const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
 #pragma unroll
@@ -544,50 +688,84 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 #pragma unroll
     for (int k = 1; k < 16; ++k)
         s += lds[k][c];
-    float sl, rest;
-    sigmoid(a.lam[j], sl, rest);
-    const float v = alone(-a.c * sl, s);
+    const float v = alone(-a.c * sigmoid(a.lam[j]), s);
     a.dlam[j] = a.accum ? a.dlam[j] + v : v;
 }
 
-template <int E>
-__device__ __forceinline__ float at(const uint8_t *row, int j)
+// The rows of one slot: whether `row` is the first of them (it takes them all, in
+// order), and `more`: whether others follow.  The wavefront looks at 64 slots a load,
+// and waits for eight loads at once.
+__device__ __forceinline__ bool first_of_slot(const int32_t *slots, int n, int row, int slot, int lane, bool &more)
 {
-    float v[1];
-    unpack<E, 1>(load<E, 1>(row + (int64_t)j * E), v);
-    return v[0];
+    bool before = false, behind = false;
+#pragma unroll 8
+    for (int k = lane; k < n; k += 64) {
+        const bool same = slots[k] == slot;
+        before = before || (same && k < row);
+        behind = behind || (same && k > row);
+    }
+    more = __any(behind);
+    return !__any(before);
 }
 
-// A wavefront a row and 64 channels.  Rows of one slot form a chain: its first
-// row takes them all, in order.
-template <int E>
-__global__ __launch_bounds__(64) void step_kernel(Args a, float *state, int64_t states, const int32_t *slots)
+// A wavefront takes a row and V channels a lane.
+template <int E, int V>
+__global__ __launch_bounds__(256) void step_kernel(Args a, float *state, int states, const int32_t *slots, int n)
 {
-    const int j = blockIdx.x * 64 + threadIdx.x;
-    const int64_t row = blockIdx.y;
-    const int64_t slot = slots ? slots[row] : row;
+    const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const int row = unit / a.columns;
+    if (row >= n)
+        return;
+    const int j = min((unit % a.columns * 64 + lane) * V, a.D - V);
+    const uint32_t off = (uint32_t)j * E;
+    Raw<E, V> x = load<E, V>(a.x + row * a.ldx + off), r = load<E, V>(a.r + row * a.ldr + off),
+              i = load<E, V>(a.i + row * a.ldi + off);
+    float rate[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        rate[v] = decay(a.lam[j + v], a.c);
+    const int slot = slots ? __builtin_amdgcn_readfirstlane(slots[row]) : row;
+    const int64_t y = (int64_t)a.D * E;
     if (slot < 0 || slot >= states) {
-        if (j < a.D)
-            store<E, 1>(a.y + (row * a.D + j) * E, {0.0f});
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            h[v] = 0.0f;
+        store<E, V>(a.y + row * y + off, h);
         return;
     }
-    if (slots) {
-        for (int64_t k = 0; k < row; ++k)
-            if (slots[k] == slot)
-                return;
-    }
-    if (j >= a.D)
+    float *s = state + (int64_t)slot * a.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        h[v] = s[(uint32_t)(j + v)];
+    bool more = false;
+    if (slots && !first_of_slot(slots, n, row, slot, lane, more))
         return;
-    const float k = decay(a.lam[j], a.c);
-    float h = state[slot * a.D + j];
-    for (int64_t t = row; t < (slots ? a.n : row + 1); ++t) {
-        if (slots && slots[t] != slot)
-            continue;
-        const Gates v = gates(at<E>(a.r + t * a.ldr, j), at<E>(a.i + t * a.ldi, j), k);
-        h = __builtin_fmaf(v.a, h, v.m * v.g * at<E>(a.x + t * a.ldx, j));
-        store<E, 1>(a.y + (t * a.D + j) * E, {h});
+    for (int t = row;;) {
+        float xf[V], rf[V], gf[V];
+        unpack<E, V>(x, xf);
+        unpack<E, V>(r, rf);
+        unpack<E, V>(i, gf);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float d, m;
+            decays<false>(rate[v] * sigmoid(rf[v]), d, m);
+            h[v] = __builtin_fmaf(d, h[v], m * sigmoid(gf[v]) * xf[v]);
+        }
+        store<E, V>(a.y + t * y + off, h);
+        if (!more)
+            break;
+        do
+            ++t;
+        while (t < n && slots[t] != slot);
+        if (t >= n)
+            break;
+        x = load<E, V>(a.x + t * a.ldx + off);
+        r = load<E, V>(a.r + t * a.ldr + off);
+        i = load<E, V>(a.i + t * a.ldi + off);
     }
-    state[slot * a.D + j] = h;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        s[(uint32_t)(j + v)] = h[v];
 }
 
 uint64_t size_of(int dtype) { return dtype == RECUR_DTYPE_F32 ? 4 : 2; }
@@ -611,7 +789,8 @@ int per_lane(int D) { return D <= 64 ? 1 : 2; }
 int64_t columns(int D) { return (D + 64 * per_lane(D) - 1) / (64 * per_lane(D)); }
 
 // Workspace: the ticket, the words of chunks and groups, the parts of dlam.
-uint64_t words_bytes(int D, int64_t n) { return align_up((uint64_t)(n + n / kGroup + 1) * D * 8); }
+int64_t words_of(int D, int64_t n) { return (n + n / kGroup + 1) * columns(D) * per_lane(D) * 64; }
+uint64_t words_bytes(int D, int64_t n) { return align_up((uint64_t)words_of(D, n) * 8); }
 uint64_t ws_need(const recur_config *c, int pass)
 {
     const int64_t n = chunks(c->max_tokens);
@@ -709,7 +888,8 @@ void place_words(Args &a, void *ws)
     uint8_t *p = (uint8_t *)ws;
     a.ticket = (uint32_t *)p;
     a.sums = (uint64_t *)(p + kAlign);
-    a.states = a.sums + (int64_t)a.chunks * a.D;
+    a.words = words_of(a.D, a.chunks);
+    a.states = a.sums + (int64_t)a.chunks * a.columns * per_lane(a.D) * 64;
     a.part = (float *)(p + kAlign + words_bytes(a.D, a.chunks));
 }
 
@@ -718,7 +898,7 @@ void clear(const Args &a, const float *in, float *out, hipStream_t s)
 {
     if (a.chunks <= 1 && !(out && (a.offsets || a.chunks == 0)))
         return;
-    const int64_t words = a.chunks > 1 ? (int64_t)(a.chunks + a.chunks / kGroup + 1) * a.D : 1;
+    const int64_t words = a.chunks > 1 ? a.words : 1;
     const unsigned grid = (unsigned)std::min<int64_t>(2048, std::max((words + 1023) / 1024, out ? a.n : 1));
     clear_kernel<<<grid, 256, 0, s>>>(a, in, out);
 }
@@ -870,7 +1050,7 @@ int recur_step(const recur_config *cfg, const recur_inputs *in, const float *lam
         return rc;
     if (!in)
         return RECUR_ENULL;
-    if (n < 0 || n > (int64_t(1) << 20) || states < 0 || states > INT32_MAX || (!slots && states < n) ||
+    if (n < 0 || n > (int64_t(1) << 16) || states < 0 || states > INT32_MAX || (!slots && states < n) ||
         bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi))
         return RECUR_ESIZE;
     if ((rc = check({strided(cfg, in->x, in->ldx, n), strided(cfg, in->r, in->ldr, n), strided(cfg, in->i, in->ldi, n),
@@ -882,9 +1062,9 @@ int recur_step(const recur_config *cfg, const recur_inputs *in, const float *lam
     Args a = base(cfg, in, lam, n);
     a.y = (uint8_t *)y;
     a.n = n;
-    const dim3 grid((cfg->dim + 63) / 64, (unsigned)n);
-    (cfg->dtype == RECUR_DTYPE_F32 ? step_kernel<4> : step_kernel<2>)<<<grid, 64, 0, (hipStream_t)stream>>>(
-        a, state, states, slots);
+    const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
+    auto k = f32 ? (one ? step_kernel<4, 1> : step_kernel<4, 2>) : (one ? step_kernel<2, 1> : step_kernel<2, 2>);
+    k<<<(unsigned)((n * a.columns + 3) / 4), 256, 0, (hipStream_t)stream>>>(a, state, (int)states, slots, (int)n);
     return done();
 }
 

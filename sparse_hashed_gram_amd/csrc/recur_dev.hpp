@@ -28,21 +28,33 @@ struct Args {
     float c;
     // workspace
     uint32_t *ticket;
-    uint64_t *sums;     // [chunks][D]: a chunk's (A, H)
-    uint64_t *states;   // [chunks / kGroup + 1][D]: the state in front of a group
+    uint64_t *sums;     // [chunks][columns][V][64]: a chunk's (A, H)
+    uint64_t *states;   // [chunks / kGroup + 1][columns][V][64]: the state in front of a group
+    int64_t words;      // of both
     float *part;        // [chunks][D]: the backward's sums for dlam
 };
+
+constexpr float kLog2e = 1.44269504f;
+
+// s(v).
+__device__ __forceinline__ float sigmoid(float v)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
+}
 
 // s(v) and 1 - s(v), neither a difference of numbers near 1.
 __device__ __forceinline__ void sigmoid(float v, float &s, float &rest)
 {
-    const float e = __expf(-fabsf(v)), q = __builtin_amdgcn_rcpf(1.0f + e), p = e * q;
+    const float e = __builtin_amdgcn_exp2f(fabsf(v) * -kLog2e), q = __builtin_amdgcn_rcpf(1.0f + e), p = e * q;
     s = v >= 0.0f ? q : p;
     rest = v >= 0.0f ? p : q;
 }
 
-// exp(z) - 1 for z <= 0: the series to z^7 above -0.35 (what it leaves out is
-// below 2^-25 of the value), else through exp, which is below 0.71 there.
+// exp(z) - 1 for z <= 0: the series to z^7 above kSeries (what it leaves out is
+// below 2^-25 of the value), else through exp, which is below 0.71 there.  ALL: z
+// is known to be above kSeries, which saves a quarter of the gates' instructions.
+constexpr float kSeries = -0.35f;
+template <bool ALL>
 __device__ __forceinline__ float expm1_neg(float z)
 {
     float p = __builtin_fmaf(z, 1.0f / 5040, 1.0f / 720);
@@ -51,11 +63,27 @@ __device__ __forceinline__ float expm1_neg(float z)
     p = __builtin_fmaf(z, p, 1.0f / 6);
     p = __builtin_fmaf(z, p, 0.5f);
     p = __builtin_fmaf(z * z, p, z);
-    return z > -0.35f ? p : __expf(z) - 1.0f;
+    if constexpr (ALL)
+        return p;
+    else
+        return z > kSeries ? p : __builtin_amdgcn_exp2f(z * kLog2e) - 1.0f;
 }
 
-// -c sp(lam), and s(lam).
-__device__ __forceinline__ float decay(float lam, float c) { return -c * (fmaxf(lam, 0.0f) + log1pf(expf(-fabsf(lam)))); }
+// -c sp(lam), sp(lam) = max(lam, 0) + log(1 + w) with w = exp(-|lam|), and log(1 + w)
+// = 2 atanh(s), s = w / (2 + w) at most 1/3: its series to s^15 leaves out less than
+// 2^-26 of the value.
+__device__ __forceinline__ float decay(float lam, float c)
+{
+    const float w = __builtin_amdgcn_exp2f(fabsf(lam) * -kLog2e), s = w * __builtin_amdgcn_rcpf(2.0f + w), q = s * s;
+    float p = __builtin_fmaf(q, 1.0f / 15, 1.0f / 13);
+    p = __builtin_fmaf(q, p, 1.0f / 11);
+    p = __builtin_fmaf(q, p, 1.0f / 9);
+    p = __builtin_fmaf(q, p, 1.0f / 7);
+    p = __builtin_fmaf(q, p, 1.0f / 5);
+    p = __builtin_fmaf(q, p, 1.0f / 3);
+    p = __builtin_fmaf(q, p, 1.0f);
+    return -c * __builtin_fmaf(2.0f * s, p, fmaxf(lam, 0.0f));
+}
 
 // a b, rounded by itself and not fused into a sum: an accumulated gradient is then
 // what was there plus the gradient that a call without accumulation gives.
@@ -70,21 +98,14 @@ __device__ __forceinline__ float alone(float a, float b)
 // registers and spills instead of 155 to 169 in the backward).
 __device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
 
-struct Gates {
-    float a, m, g, g_rest, rho, rho_rest;
-};
-
-// a = 1 + e and 1 - a^2 = -e (2 + e) with e = exp(z) - 1, so that both keep their
-// relative precision where a is near 1.
-__device__ __forceinline__ Gates gates(float r, float i, float k)
+// a = 1 + e and m = sqrt(1 - a^2) = sqrt(-e (2 + e)) with e = exp(z) - 1, so that
+// both keep their relative precision where a is near 1.
+template <bool ALL>
+__device__ __forceinline__ void decays(float z, float &a, float &m)
 {
-    Gates t;
-    sigmoid(r, t.rho, t.rho_rest);
-    sigmoid(i, t.g, t.g_rest);
-    const float e = expm1_neg(k * t.rho);
-    t.a = 1.0f + e;
-    t.m = __builtin_amdgcn_sqrtf(-e * (2.0f + e));
-    return t;
+    const float e = expm1_neg<ALL>(z);
+    a = 1.0f + e;
+    m = __builtin_amdgcn_sqrtf(-e * (2.0f + e));
 }
 
 // V channels side by side as floats.  Rows start at any element: the access

@@ -147,7 +147,7 @@ def test_step_refusals(M):
     assert L.recur_step(c, None, A[3], A[4], 4, None, 4, A[6], None) == -1
     for k in ("lam", "state", "slots"):
         assert call(**{k: A[7] + 2}) == -2, k
-    assert call(n=-1) == -4 and call(n=(1 << 20) + 1) == -4 and call(states=-1) == -4 and call(ldx=63) == -4
+    assert call(n=-1) == -4 and call(n=(1 << 16) + 1) == -4 and call(states=-1) == -4 and call(ldx=63) == -4
     assert call(slots=None, states=19) == -4
     for k in ("y", "state"):
         for bad in (A[0], A[1] + 64, A[3], A[5]):
