@@ -43,12 +43,12 @@ __device__ __forceinline__ float param_at(const uint8_t *p, int f32, int one, in
                : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(p)[j] << 16);
 }
 
-// Column sums over the parts, in a fixed order: 64 columns a block, 16 threads to
+// Column sums over the parts, in a fixed order: 16 columns a block, 64 threads to
 // a column.  blockIdx.y: the norm in front, the norm and gate behind, the scale.
 __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
 {
-    __shared__ float lds[2][16][64];
-    const int c = threadIdx.x % 64, g = threadIdx.x / 64, j = blockIdx.x * 64 + c;
+    __shared__ float lds[2][64][16];
+    const int c = threadIdx.x % 16, g = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     const int ld = (a.D + 3) / 4 * 4, what = blockIdx.y;
     const int first = what == 0 ? kSumPreW : what == 1 ? kSumPost1 : kSumScale;
     const int second = what == 0 ? (a.db ? kSumPreB : -1)
@@ -57,8 +57,8 @@ __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
     if (j < a.D) {
         const float *p = a.part + (int64_t)g * kSums * ld + j + first * ld;
         const int apart = second >= 0 ? (second - first) * ld : 0;
-#pragma unroll 16
-        for (int i = g; i < a.parts; i += 16, p += 16 * kSums * ld) {
+#pragma unroll 8
+        for (int i = g; i < a.parts; i += 64, p += 64 * kSums * ld) {
             x += p[0];
             y += p[apart];
         }
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
     if (g != 0 || j >= a.D)
         return;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < 64; ++i) {
         x += lds[0][i][c];
         y += lds[1][i][c];
     }
@@ -237,7 +237,7 @@ int gradients(const norm_config *c, const Args &a, const norm_grads &g, int part
     const bool post = d.dpost_w || d.dpost_b || d.dgate;
     if (!d.dw && !d.db && !post && !d.dscale)
         return done();
-    const dim3 grid((c->dim + 63) / 64, d.dscale ? 3 : post ? 2 : 1);
+    const dim3 grid((c->dim + 15) / 16, d.dscale ? 3 : post ? 2 : 1);
     grad_kernel<<<grid, 1024, 0, s>>>(d);
     if ((d.dgate && d.p.gate_one) || (d.dscale && d.p.scale_one))
         scalar_kernel<<<2, 256, 0, s>>>(d);

@@ -18,52 +18,56 @@ using spans::meet;
 using spans::Span;
 
 constexpr uint64_t kAlign = 256;
-constexpr int kThreads = kWaves * 64;
 
-// Where sequences begin and end among a chunk's positions.
+// Where sequences begin and end among the positions of a block's wavefronts: bit k is
+// a wavefront's position k.
+template <int WAVES, int STEPS>
 struct Marks {
-    unsigned long long starts, ends;
-    int start_of[kChunk], end_of[kChunk];   // the sequence, where the bit is set
+    uint32_t starts[WAVES], ends[WAVES];
+    int start_of[WAVES][STEPS], end_of[WAVES][STEPS];   // the sequence, where the bit is set
 };
 
-// A wavefront's view of them: bit k is its position k.
+// A wavefront's view of them, and which of its positions belong to a sequence.
 struct Bits {
     uint32_t starts, ends, inside;
 };
 
 // All threads of the block.  The sequences that can matter: those from the last
 // probe that begins in front of t0 to the first that begins behind the chunk.
-__device__ void find_marks(const Args &a, int64_t t0, Marks *m)
+template <int WAVES, int STEPS>
+__device__ void find_marks(const Args &a, int64_t t0, Marks<WAVES, STEPS> *m)
 {
+    constexpr int threads = WAVES * 64, N = WAVES * STEPS;
     __shared__ int from, to;
+    if (threadIdx.x < WAVES)
+        m->starts[threadIdx.x] = m->ends[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
-        m->starts = m->ends = 0;
         from = 0;
         to = (int)a.n;
     }
     __syncthreads();
-    if (a.n > 4 * kThreads) {
-        const int64_t step = (a.n + kThreads - 1) / kThreads, at = threadIdx.x * step;
+    if (a.n > 4 * threads) {
+        const int64_t step = (a.n + threads - 1) / threads, at = threadIdx.x * step;
         if (at < a.n) {
             const int32_t v = a.offsets[at];
             if (v < t0)
                 atomicMax(&from, (int)at);
-            if (v > t0 + kChunk)
+            if (v > t0 + N)
                 atomicMin(&to, (int)at);
         }
         __syncthreads();
     }
-    for (int s = from + (int)threadIdx.x; s < to; s += kThreads) {
-        const int64_t b = a.offsets[s], e = a.offsets[s + 1];
-        if (b >= e)
+    for (int s = from + (int)threadIdx.x; s < to; s += threads) {
+        const int64_t b = a.offsets[s] - t0, e = a.offsets[s + 1] - t0 - 1;   // first and last position
+        if (b > e)
             continue;
-        if (b >= t0 && b < t0 + kChunk) {
-            atomicOr(&m->starts, 1ull << (b - t0));
-            m->start_of[b - t0] = s;
+        if (b >= 0 && b < N) {
+            atomicOr(&m->starts[b / STEPS], 1u << (b % STEPS));
+            m->start_of[b / STEPS][b % STEPS] = s;
         }
-        if (e > t0 && e <= t0 + kChunk) {
-            atomicOr(&m->ends, 1ull << (e - 1 - t0));
-            m->end_of[e - 1 - t0] = s;
+        if (e >= 0 && e < N) {
+            atomicOr(&m->ends[e / STEPS], 1u << (e % STEPS));
+            m->end_of[e / STEPS][e % STEPS] = s;
         }
     }
     __syncthreads();
@@ -77,7 +81,7 @@ __device__ __forceinline__ void place(const Args &a, int &chunk, int &column)
     __shared__ uint32_t ticket;
     chunk = 0;
     column = blockIdx.x;
-    if (a.chunks > 1) {
+    if (!a.alone) {
         if (threadIdx.x == 0)
             ticket = atomicAdd(a.ticket, 1u);
         __syncthreads();
@@ -90,37 +94,42 @@ __device__ __forceinline__ void place(const Args &a, int &chunk, int &column)
 __device__ __forceinline__ void rows_of_sequences(const Args &a, int64_t &lo, int64_t &hi)
 {
     lo = a.offsets ? max((int64_t)0, (int64_t)a.offsets[0]) : 0;
-    hi = a.offsets ? min(a.T, (int64_t)a.offsets[a.n]) : a.T;
+    hi = a.offsets ? max((int64_t)0, min(a.T, (int64_t)a.offsets[a.n])) : a.T;
 }
 
-__device__ __forceinline__ Bits bits_of(const Args &a, const Marks *m, int64_t t0, int64_t lo, int64_t hi, int wave)
+// t: the wavefront's first position.
+template <int WAVES, int STEPS>
+__device__ __forceinline__ Bits bits_of(const Args &a, const Marks<WAVES, STEPS> &m, int64_t t, int64_t lo, int64_t hi,
+                                        int wave)
 {
     Bits b;
-    const int64_t t = t0 + wave * kSteps;
     if (a.offsets) {
-        b.starts = (uint32_t)(m->starts >> (wave * kSteps)) & ((1u << kSteps) - 1);
-        b.ends = (uint32_t)(m->ends >> (wave * kSteps)) & ((1u << kSteps) - 1);
+        b.starts = m.starts[wave];
+        b.ends = m.ends[wave];
     } else {
         b.starts = t == 0 ? 1u : 0u;
-        b.ends = hi > t && hi <= t + kSteps ? 1u << (hi - 1 - t) : 0u;
+        b.ends = hi > t && hi <= t + STEPS ? 1u << (hi - 1 - t) : 0u;
     }
-    b.inside = 0;
+    b.inside = (1u << STEPS) - 1;
+    if (t < lo || t + STEPS > hi) {
+        b.inside = 0;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-        b.inside |= (t + k >= lo && t + k < hi ? 1u : 0u) << k;
+        for (int k = 0; k < STEPS; ++k)
+            b.inside |= (t + k >= lo && t + k < hi ? 1u : 0u) << k;
+    }
     b.starts = __builtin_amdgcn_readfirstlane(b.starts & b.inside);
     b.ends = __builtin_amdgcn_readfirstlane(b.ends & b.inside);
     b.inside = __builtin_amdgcn_readfirstlane(b.inside);
     return b;
 }
 
-template <int V>
+template <int V, int WAVES, int STEPS>
 struct Shared {
-    Span1 waves[kWaves][V][64];   // each wavefront's stretch
-    Span1 before[kWaves][V][64];  // stretches of the chunks before, kGroup / kWaves a wavefront
+    Span1 waves[WAVES][V][64];    // each wavefront's stretch
+    Span1 before[WAVES][V][64];   // stretches of the chunks before, some to a wavefront
     Span1 all[V][64];             // the chunk
     float state[V][64];           // the state in front of the group of chunks
-    Marks marks;
+    Marks<WAVES, STEPS> marks;
 };
 
 // The state in front of the block's chunk; `index` counts chunks in the order in
@@ -140,16 +149,16 @@ constexpr int kPolls = 1 << 20;
 __device__ __forceinline__ uint64_t wait_for(const uint64_t *p, uint64_t w)
 {
     for (int polls = 0; polls < kPolls && __any(w == kNone); ++polls) {
-        __builtin_amdgcn_s_sleep(4);
+        __builtin_amdgcn_s_sleep(1);
         if (w == kNone)
             w = peek(p);
     }
     return w;
 }
 
-template <int V>
-__device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int index, int column, int wave, int order,
-                                             int lane, const Span1 (&own)[V], float (&h)[V])
+template <int V, int WAVES, int STEPS>
+__device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STEPS> &sh, int chunks, int index, int column,
+                                             int wave, int order, int lane, const Span1 (&own)[V], float (&h)[V])
 {
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -158,18 +167,18 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
 #pragma unroll
     for (int v = 0; v < V; ++v)
         h[v] = 0.0f;
-    if (a.chunks <= 1)
+    if (chunks <= 1)
         return;
-    constexpr int per = kGroup / kWaves;
+    constexpr int per = (kGroup + WAVES - 1) / WAVES;
     const int group = index / kGroup, place = index % kGroup;
     const int64_t step = (int64_t)a.columns * V * 64;   // words of a chunk
     const int at = column * V * 64 + lane;
-    if (wave == kWaves - 1) {
+    if (wave == WAVES - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             Span1 all = sh.waves[0][v][lane];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < WAVES; ++w)
                 all = join(all, sh.waves[w][v][lane]);
             publish(&a.sums[index * step + at + v * 64], word(all));
             sh.all[v][lane] = all;
@@ -178,6 +187,9 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
     if (place > 0) {
         const uint64_t *p = a.sums + ((int64_t)group * kGroup + wave * per) * step + at;
         const int mine = min(per, place - wave * per);   // chunks before that this wavefront looks at
+        const bool asks = wave == WAVES - 1 && group > 0;
+        const uint64_t *q = a.states + group * step + at;
+        uint64_t first[V];
         uint64_t w[per][V];
 #pragma unroll
         for (int i = 0; i < per; ++i)
@@ -185,6 +197,10 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     w[i][v] = peek(p + i * step + v * 64);
+        if (asks)   // mostly there by now
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                first[v] = peek(q + v * 64);
         Span1 s[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -207,11 +223,11 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
             for (int v = 0; v < V; ++v)
                 s[v] = join(s[v], sh.before[i][v][lane]);
         if (group > 0 || place == kGroup - 1) {
-            if (wave == kWaves - 1) {
+            if (wave == WAVES - 1) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    h[v] = group > 0 ? span(wait_for(a.states + group * step + at + v * 64, kNone)).H : 0.0f;
-                if (place == kGroup - 1 && index + 1 < a.chunks) {
+                    h[v] = asks ? span(wait_for(q + v * 64, first[v])).H : 0.0f;
+                if (place == kGroup - 1 && index + 1 < chunks) {
 #pragma unroll
                     for (int v = 0; v < V; ++v)
                         publish(a.states + (group + 1) * step + at + v * 64,
@@ -230,7 +246,7 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
         for (int v = 0; v < V; ++v)
             h[v] = through(s[v], h[v]);
     } else if (group > 0) {
-        if (wave == kWaves - 1) {
+        if (wave == WAVES - 1) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 sh.state[v][lane] = span(wait_for(a.states + group * step + at + v * 64, kNone)).H;
@@ -247,10 +263,10 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V> &sh, int i
 __global__ __launch_bounds__(256) void clear_kernel(Args a, const float *in, float *out)
 {
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-    if (a.chunks > 1) {
-        const int64_t words = a.words;   // sums, then states
-        for (int64_t k = first; k < words; k += step)
-            a.sums[k] = kNone;
+    if (!a.alone) {
+        ulonglong2 *sums = reinterpret_cast<ulonglong2 *>(a.sums);   // sums, then states: a multiple of 64 words
+        for (int64_t k = first; k < a.words / 2; k += step)
+            sums[k] = make_ulonglong2(kNone, kNone);
         if (first == 0)
             *a.ticket = 0;
     }
@@ -265,32 +281,32 @@ __global__ __launch_bounds__(256) void clear_kernel(Args a, const float *in, flo
     }
 }
 
-// kSteps rows from t on; rows behind the last are the last again.
-template <int E, int V>
+// STEPS rows from t on; rows behind the last are the last again.
+template <int E, int V, int STEPS>
 __device__ __forceinline__ void load_rows(const uint8_t *p, int64_t ld, int64_t t, int64_t T, uint32_t off,
-                                          Raw<E, V> (&v)[kSteps])
+                                          Raw<E, V> (&v)[STEPS])
 {
     p += t * ld;
-    if (t + kSteps <= T) {
+    if (t + STEPS <= T) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             v[k] = load<E, V>(p + off);
             p += ld;
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < STEPS; ++k)
             v[k] = load<E, V>(p + (min(t + k, T - 1) - t) * ld + off);
     }
 }
 
 template <int E, int V, bool ALL>
-__device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kSteps], const Raw<E, V> (&r)[kSteps],
-                                          const Raw<E, V> (&i)[kSteps], const float (&rate)[V], float (&av)[kSteps][V],
-                                          float (&u)[kSteps][V])
+__device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kFwdSteps], const Raw<E, V> (&r)[kFwdSteps],
+                                          const Raw<E, V> (&i)[kFwdSteps], const float (&rate)[V], float (&av)[kFwdSteps][V],
+                                          float (&u)[kFwdSteps][V])
 {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
+    for (int k = 0; k < kFwdSteps; ++k) {
         float xf[V], rf[V], gf[V];
         unpack<E, V>(x[k], xf);
         unpack<E, V>(r[k], rf);
@@ -300,25 +316,29 @@ __device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kSteps], const Ra
             float m;
             decays<ALL>(rate[v] * sigmoid(rf[v]), av[k][v], m);
             u[k][v] = m * sigmoid(gf[v]) * xf[v];
+            here(av[k][v]);
+            here(u[k][v]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 template <int E, int V>
-__global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
+__global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Args a)
 {
-    __shared__ Shared<V> sh;
+    constexpr int WAVES = kFwdWaves, STEPS = kFwdSteps;
+    __shared__ Shared<V, WAVES, STEPS> sh;
     int chunk, column;
     place(a, chunk, column);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     // lanes past the last channels take those again: the same loads, values and stores
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;   // behind a row's address, which is the same for all lanes
-    const int64_t t0 = (int64_t)chunk * kChunk, t = t0 + wave * kSteps;
-    Raw<E, V> x[kSteps], r[kSteps], i[kSteps];
-    load_rows<E, V>(a.r, a.ldr, t, a.T, off, r);
-    load_rows<E, V>(a.i, a.ldi, t, a.T, off, i);
-    load_rows<E, V>(a.x, a.ldx, t, a.T, off, x);
+    const int64_t t0 = (int64_t)chunk * kFwdChunk, t = t0 + wave * STEPS;
+    Raw<E, V> x[STEPS], r[STEPS], i[STEPS];
+    load_rows<E, V, STEPS>(a.r, a.ldr, t, a.T, off, r);
+    load_rows<E, V, STEPS>(a.i, a.ldi, t, a.T, off, i);
+    load_rows<E, V, STEPS>(a.x, a.ldx, t, a.T, off, x);
     float rate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -328,10 +348,10 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
     if (t0 >= hi)
         return;   // nor does any chunk behind it ask
     if (a.offsets)
-        find_marks(a, t0, &sh.marks);
-    const Bits bits = bits_of(a, &sh.marks, t0, lo, hi, wave);
-    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << kSteps) - 1;
-    float av[kSteps][V], u[kSteps][V];
+        find_marks<WAVES, STEPS>(a, t0, &sh.marks);
+    const Bits bits = bits_of<WAVES, STEPS>(a, sh.marks, t, lo, hi, wave);
+    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << STEPS) - 1;
+    float av[STEPS][V], u[STEPS][V];
     bool all = true;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -346,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
         own[v] = Span1{1.0f, 0.0f};
     if (plain) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k)
+        for (int k = 0; k < STEPS; ++k)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 own[v].A *= av[k][v];
@@ -354,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
             }
     } else {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             const bool start = bits.starts >> k & 1, inside = bits.inside >> k & 1;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -362,7 +382,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
                 u[k][v] = inside ? u[k][v] : 0.0f;
             }
             if (start && a.h0) {
-                const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
+                const int64_t s = a.offsets ? sh.marks.start_of[wave][k] : 0;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     u[k][v] = __builtin_fmaf(av[k][v], a.h0[s * a.D + j + v], u[k][v]);
@@ -380,20 +400,26 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
         }
     }
     float h[V];
-    state_before<V>(a, sh, chunk, column, wave, wave, lane, own, h);
-    if (a.saved && wave == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            a.saved[(int64_t)chunk * a.D + j + v] = h[v];
-    }
+    state_before<V, WAVES, STEPS>(a, sh, (int)((hi + kFwdChunk - 1) / kFwdChunk), chunk, column, wave, wave, lane, own, h);
     for (int w = 0; w < wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             h[v] = through(sh.waves[w][v][lane], h[v]);
+    // the wavefront's position in front of which a state is saved, if one is: RECUR_CHUNK >= STEPS
+    const int keep = a.saved ? (int)((RECUR_CHUNK - t % RECUR_CHUNK) % RECUR_CHUNK) : STEPS;
+    float *saved = a.saved + (t + keep) / RECUR_CHUNK * a.D + j;
+    auto save = [&](int k) {
+        if (k == keep && t + k < a.T) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                saved[v] = h[v];
+        }
+    };
     uint8_t *y = a.y + t * a.D * E;
     if (plain) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
+            save(k);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = __builtin_fmaf(av[k][v], h[v], u[k][v]);
@@ -402,7 +428,8 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
+            save(k);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = bits.starts >> k & 1 ? u[k][v] : __builtin_fmaf(av[k][v], h[v], u[k][v]);
@@ -410,7 +437,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
                 store<E, V>(y + off, h);
             y += (int64_t)a.D * E;
             if (a.hT && (bits.ends >> k & 1)) {
-                const int64_t s = a.offsets ? sh.marks.end_of[wave * kSteps + k] : 0;
+                const int64_t s = a.offsets ? sh.marks.end_of[wave][k] : 0;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     a.hT[s * a.D + j + v] = h[v];
@@ -420,10 +447,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
 }
 
 // The sequence that begins or ends at the wavefront's position k.
-__device__ __forceinline__ int64_t sequence_of(const Args &a, const int (&of)[kChunk], int wave, int k)
-{
-    return a.offsets ? of[wave * kSteps + k] : 0;
-}
+__device__ __forceinline__ int64_t sequence_of(const Args &a, const int *of, int k) { return a.offsets ? of[k] : 0; }
 
 // H = the sequence's row of h0 or dhT, 0 without them.
 template <int V>
@@ -437,13 +461,13 @@ __device__ __forceinline__ void row_of(const float *p, int64_t sequence, int D, 
 // A position's numbers that need no state: a, m g (dx / G), m g x (1 - g) (di / G), and
 // of dz / G the part beside a h_{t-1}: g x a^2 / m.
 template <int E, int V, bool ALL>
-__device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kSteps], const Raw<E, V> (&r)[kSteps],
-                                          const Raw<E, V> (&i)[kSteps], const float (&rate)[V], float (&av)[kSteps][V],
-                                          float (&c1)[kSteps][V], float (&c2)[kSteps][V],
-                                          float (&c3)[kSteps][V], float (&cr)[kSteps][V], float (&cl)[kSteps][V])
+__device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const Raw<E, V> (&r)[kBwdSteps],
+                                          const Raw<E, V> (&i)[kBwdSteps], const float (&rate)[V], float (&av)[kBwdSteps][V],
+                                          float (&c1)[kBwdSteps][V], float (&c2)[kBwdSteps][V],
+                                          float (&c3)[kBwdSteps][V], float (&cr)[kBwdSteps][V], float (&cl)[kBwdSteps][V])
 {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
+    for (int k = 0; k < kBwdSteps; ++k) {
         float xf[V], rf[V], gf[V];
         unpack<E, V>(x[k], xf);
         unpack<E, V>(r[k], rf);
@@ -459,7 +483,8 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kSteps], const Ra
             c2[k][v] = c1[k][v] * xf[v] * g_rest;
             cl[k][v] = rho;
             cr[k][v] = z * rho_rest;
-            c3[k][v] = m > 0.0f ? g * xf[v] * (av[k][v] * av[k][v] * __builtin_amdgcn_rcpf(m)) : 0.0f;
+            // where m is 0, z is too, and with it what this is multiplied by
+            c3[k][v] = g * xf[v] * (av[k][v] * av[k][v] * __builtin_amdgcn_rcpf(fmaxf(m, 1e-18f)));
             here(c1[k][v]);
             here(c2[k][v]);
             here(c3[k][v]);
@@ -474,34 +499,37 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kSteps], const Ra
 // its position: dx c1, di c2, dr cr, and rho dz (of dlam) cl.  G in turn runs
 // backwards, what a position hands on being a_t G_t.
 template <int E, int V>
-__global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
+__global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Args a)
 {
-    __shared__ Shared<V> sh;
+    constexpr int WAVES = kBwdWaves, STEPS = kBwdSteps;
+    __shared__ Shared<V, WAVES, STEPS> sh;
     int index, column;
     place(a, index, column);
-    const int chunk = a.chunks - 1 - index;
+    int64_t lo, hi;
+    rows_of_sequences(a, lo, hi);
+    const int chunks = (int)((hi + kBwdChunk - 1) / kBwdChunk), chunk = chunks - 1 - index;
+    if (chunk < 0)
+        return;   // behind the last sequence: as many blocks as chunks are left
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;
-    const int64_t t0 = (int64_t)chunk * kChunk, t = t0 + wave * kSteps;
-    Raw<E, V> x[kSteps], r[kSteps], i[kSteps], d[kSteps];
-    load_rows<E, V>(a.r, a.ldr, t, a.T, off, r);
-    load_rows<E, V>(a.i, a.ldi, t, a.T, off, i);
-    load_rows<E, V>(a.x, a.ldx, t, a.T, off, x);
-    load_rows<E, V>(a.dy, (int64_t)a.D * E, t, a.T, off, d);
+    const int64_t t0 = (int64_t)chunk * kBwdChunk, t = t0 + wave * STEPS;
+    Raw<E, V> x[STEPS], r[STEPS], i[STEPS], d[STEPS];
+    load_rows<E, V, STEPS>(a.r, a.ldr, t, a.T, off, r);
+    load_rows<E, V, STEPS>(a.i, a.ldi, t, a.T, off, i);
+    load_rows<E, V, STEPS>(a.x, a.ldx, t, a.T, off, x);
+    load_rows<E, V, STEPS>(a.dy, (int64_t)a.D * E, t, a.T, off, d);
     float rate[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         rate[v] = decay(a.lam[j + v], a.c);
         h[v] = a.saved[(int64_t)chunk * a.D + j + v];
     }
-    int64_t lo, hi;
-    rows_of_sequences(a, lo, hi);
     if (a.offsets)
-        find_marks(a, t0, &sh.marks);
-    const Bits bits = bits_of(a, &sh.marks, t0, lo, hi, wave);
-    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << kSteps) - 1;
-    float av[kSteps][V], c1[kSteps][V], c2[kSteps][V], c3[kSteps][V], cr[kSteps][V], cl[kSteps][V];
+        find_marks<WAVES, STEPS>(a, t0, &sh.marks);
+    const Bits bits = bits_of<WAVES, STEPS>(a, sh.marks, t, lo, hi, wave);
+    const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << STEPS) - 1;
+    float av[STEPS][V], c1[STEPS][V], c2[STEPS][V], c3[STEPS][V], cr[STEPS][V], cl[STEPS][V];
     bool all = true;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -520,7 +548,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
     }
     if (plain) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             float xf[V];
             unpack<E, V>(x[k], xf);
 #pragma unroll
@@ -530,7 +558,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
             }
         }
 #pragma unroll
-        for (int k = kSteps - 1; k >= 0; --k) {
+        for (int k = STEPS - 1; k >= 0; --k) {
             float df[V];
             unpack<E, V>(d[k], df);
 #pragma unroll
@@ -542,7 +570,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
             back[v].A = own[v].A;
     } else {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+        for (int k = 0; k < STEPS; ++k) {
             if (!(bits.inside >> k & 1)) {
                 x[k].w = d[k].w = 0;
 #pragma unroll
@@ -550,7 +578,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
                     av[k][v] = 1.0f;
             }
             if (bits.starts >> k & 1)
-                row_of<V>(a.h0, sequence_of(a, sh.marks.start_of, wave, k), a.D, j, own);
+                row_of<V>(a.h0, sequence_of(a, sh.marks.start_of[wave], k), a.D, j, own);
             float xf[V];
             unpack<E, V>(x[k], xf);
 #pragma unroll
@@ -560,9 +588,9 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
             }
         }
 #pragma unroll
-        for (int k = kSteps - 1; k >= 0; --k) {
+        for (int k = STEPS - 1; k >= 0; --k) {
             if (bits.ends >> k & 1)
-                row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of, wave, k), a.D, j, back);
+                row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of[wave], k), a.D, j, back);
             float df[V];
             unpack<E, V>(d[k], df);
 #pragma unroll
@@ -585,9 +613,9 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
         for (int v = 0; v < V; ++v)
             h[v] = through(sh.before[w][v][lane], h[v]);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
+    for (int k = 0; k < STEPS; ++k) {
         if (bits.starts >> k & 1) {
-            row_of<V>(a.h0, sequence_of(a, sh.marks.start_of, wave, k), a.D, j, own);
+            row_of<V>(a.h0, sequence_of(a, sh.marks.start_of[wave], k), a.D, j, own);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h[v] = own[v].H;
@@ -605,20 +633,20 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
         }
     }
     float in[V], acc[V];
-    state_before<V>(a, sh, index, column, wave, kWaves - 1 - wave, lane, back, in);
-    for (int w = 0; w < kWaves - 1 - wave; ++w)
+    state_before<V, WAVES, STEPS>(a, sh, chunks, index, column, wave, WAVES - 1 - wave, lane, back, in);
+    for (int w = 0; w < WAVES - 1 - wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             in[v] = through(sh.waves[w][v][lane], in[v]);
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.0f;
-    uint8_t *px = a.dx + (t + kSteps - 1) * a.lddx, *pr = a.dr + (t + kSteps - 1) * a.lddr,
-            *pi = a.di + (t + kSteps - 1) * a.lddi;
+    uint8_t *px = a.dx + (t + STEPS - 1) * a.lddx, *pr = a.dr + (t + STEPS - 1) * a.lddr,
+            *pi = a.di + (t + STEPS - 1) * a.lddi;
 #pragma unroll
-    for (int k = kSteps - 1; k >= 0; --k) {
+    for (int k = STEPS - 1; k >= 0; --k) {
         if (bits.ends >> k & 1) {
-            row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of, wave, k), a.D, j, own);
+            row_of<V>(a.dhT, sequence_of(a, sh.marks.end_of[wave], k), a.D, j, own);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 in[v] = own[v].H;
@@ -646,7 +674,7 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
         pr -= a.lddr;
         pi -= a.lddi;
         if (a.dh0 && (bits.starts >> k & 1)) {
-            const int64_t s = a.offsets ? sh.marks.start_of[wave * kSteps + k] : 0;
+            const int64_t s = a.offsets ? sh.marks.start_of[wave][k] : 0;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 a.dh0[s * a.D + j + v] = in[v];
@@ -662,23 +690,26 @@ __global__ __launch_bounds__(kThreads) void bwd_kernel(Args a)
         for (int v = 0; v < V; ++v) {
             float s = sh.waves[0][v][lane].A;
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < WAVES; ++w)
                 s += sh.waves[w][v][lane].A;
             a.part[(int64_t)chunk * a.D + j + v] = s;
         }
     }
 }
 
-// dlam from the chunks' parts, in a fixed order: 64 channels a block, 16 threads to
+// dlam from the chunks' parts, in a fixed order: 16 channels a block, 64 threads to
 // a channel.
 __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 {
-    __shared__ float lds[16][64];
-    const int c = threadIdx.x % 64, g = threadIdx.x / 64, j = blockIdx.x * 64 + c;
+    __shared__ float lds[64][16];
+    const int c = threadIdx.x % 16, g = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     float s = 0.0f;
-    if (j < a.D) {
-#pragma unroll 8
-        for (int64_t k = g; k < a.chunks; k += 16)
+    if (j < a.D && a.T > 0) {
+        int64_t lo, hi;
+        rows_of_sequences(a, lo, hi);
+        const int64_t chunks = (hi + kBwdChunk - 1) / kBwdChunk;
+#pragma unroll 16
+        for (int64_t k = g; k < chunks; k += 64)
             s += a.part[k * a.D + j];
     }
     lds[g][c] = s;
@@ -686,7 +717,7 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
     if (g != 0 || j >= a.D)
         return;
 #pragma unroll
-    for (int k = 1; k < 16; ++k)
+    for (int k = 1; k < 64; ++k)
         s += lds[k][c];
     const float v = alone(-a.c * sigmoid(a.lam[j]), s);
     a.dlam[j] = a.accum ? a.dlam[j] + v : v;
@@ -780,7 +811,12 @@ int check_config(const recur_config *c)
     return ok ? RECUR_OK : RECUR_ECONFIG;
 }
 
-int64_t chunks(int64_t T) { return (T + kChunk - 1) / kChunk; }
+int64_t saved_rows(int64_t T) { return (T + RECUR_CHUNK - 1) / RECUR_CHUNK; }
+int64_t chunks(int pass, int64_t T)
+{
+    const int n = pass == RECUR_PASS_FWD ? kFwdChunk : kBwdChunk;
+    return (T + n - 1) / n;
+}
 uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // A lane takes two channels; up to 64 channels one, or half the wavefront would
@@ -788,13 +824,13 @@ uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 int per_lane(int D) { return D <= 64 ? 1 : 2; }
 int64_t columns(int D) { return (D + 64 * per_lane(D) - 1) / (64 * per_lane(D)); }
 
-// Workspace: the ticket, the words of chunks and groups, the parts of dlam.
-int64_t words_of(int D, int64_t n) { return (n + n / kGroup + 1) * columns(D) * per_lane(D) * 64; }
-uint64_t words_bytes(int D, int64_t n) { return align_up((uint64_t)words_of(D, n) * 8); }
+// Workspace: the ticket, the words of n chunks and their groups, the backward's
+// parts of dlam.
+uint64_t words_of(int D, int64_t n) { return (uint64_t)(n + n / kGroup + 1) * columns(D) * per_lane(D) * 64; }
 uint64_t ws_need(const recur_config *c, int pass)
 {
-    const int64_t n = chunks(c->max_tokens);
-    return kAlign + words_bytes(c->dim, n) + (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
+    const int64_t n = chunks(pass, c->max_tokens);
+    return kAlign + align_up(words_of(c->dim, n) * 8) + (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
 }
 
 struct Buf {
@@ -858,7 +894,7 @@ int check_call(const recur_config *cfg, int pass, const void *ws, uint64_t ws_by
         return RECUR_EALIGN;
     if (T < 0 || T > cfg->max_tokens || n < 0 || n > (int64_t(1) << 24) || (!offsets && n != 1) ||
         bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi) || ws_bytes < ws_need(cfg, pass) ||
-        chunks(T) * columns(cfg->dim) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
+        chunks(pass, T) * columns(cfg->dim) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
         return RECUR_ESIZE;
     return RECUR_OK;
 }
@@ -878,28 +914,29 @@ Args base(const recur_config *c, const recur_inputs *in, const float *lam, int64
     a.D = c->dim;
     a.c = c->c;
     a.accum = (c->options & RECUR_OPT_ACCUM) != 0;
-    a.chunks = (int)chunks(T);
     a.columns = (int)columns(c->dim);
     return a;
 }
 
-void place_words(Args &a, void *ws)
+void place_words(Args &a, int pass, void *ws)
 {
     uint8_t *p = (uint8_t *)ws;
+    const int64_t n = chunks(pass, a.T);
+    a.alone = n <= 1;
+    a.words = (int64_t)words_of(a.D, n);
     a.ticket = (uint32_t *)p;
     a.sums = (uint64_t *)(p + kAlign);
-    a.words = words_of(a.D, a.chunks);
-    a.states = a.sums + (int64_t)a.chunks * a.columns * per_lane(a.D) * 64;
-    a.part = (float *)(p + kAlign + words_bytes(a.D, a.chunks));
+    a.states = a.sums + n * a.columns * per_lane(a.D) * 64;
+    a.part = (float *)(p + kAlign + align_up((uint64_t)a.words * 8));
 }
 
 // What has to be done before the chunks; states without rows: out = in.
 void clear(const Args &a, const float *in, float *out, hipStream_t s)
 {
-    if (a.chunks <= 1 && !(out && (a.offsets || a.chunks == 0)))
+    if (a.alone && !(out && (a.offsets || a.T == 0)))
         return;
-    const int64_t words = a.chunks > 1 ? a.words : 1;
-    const unsigned grid = (unsigned)std::min<int64_t>(2048, std::max((words + 1023) / 1024, out ? a.n : 1));
+    const int64_t words = a.alone ? 1 : a.words;
+    const unsigned grid = (unsigned)std::min<int64_t>(2048, std::max((words + 2047) / 2048, out ? a.n : 1));
     clear_kernel<<<grid, 256, 0, s>>>(a, in, out);
 }
 
@@ -952,7 +989,7 @@ int recur_saved_bytes(const recur_config *cfg, int64_t T, uint64_t *bytes)
         return RECUR_ENULL;
     if (T < 0 || T > cfg->max_tokens)
         return RECUR_ESIZE;
-    *bytes = (uint64_t)chunks(T) * cfg->dim * 4;
+    *bytes = (uint64_t)saved_rows(T) * cfg->dim * 4;
     return RECUR_OK;
 }
 
@@ -966,7 +1003,7 @@ int recur_fwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     if ((rc = check({strided(cfg, in->x, in->ldx, T), strided(cfg, in->r, in->ldr, T), strided(cfg, in->i, in->ldi, T),
                      states_of(cfg, lam, 1, true), Buf{Span{offsets, offsets ? 4 * ((uint64_t)n + 1) : 0}, 4, false},
                      states_of(cfg, h0, n)},
-                    {rows_of(cfg, y, T), states_of(cfg, hT, n), states_of(cfg, saved, chunks(T))}, Span{ws, ws_bytes})))
+                    {rows_of(cfg, y, T), states_of(cfg, hT, n), states_of(cfg, saved, saved_rows(T))}, Span{ws, ws_bytes})))
         return rc;
     if (n == 0 || (T == 0 && !hT))
         return RECUR_OK;
@@ -977,13 +1014,13 @@ int recur_fwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     a.y = (uint8_t *)y;
     a.hT = hT;
     a.saved = saved;
-    place_words(a, ws);
+    place_words(a, RECUR_PASS_FWD, ws);
     hipStream_t s = (hipStream_t)stream;
     clear(a, h0, hT, s);
     if (T) {
         const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
         auto k = f32 ? (one ? fwd_kernel<4, 1> : fwd_kernel<4, 2>) : (one ? fwd_kernel<2, 1> : fwd_kernel<2, 2>);
-        k<<<(unsigned)(a.chunks * (int64_t)a.columns), kThreads, 0, s>>>(a);
+        k<<<(unsigned)(chunks(RECUR_PASS_FWD, T) * a.columns), kFwdWaves * 64, 0, s>>>(a);
     }
     return done();
 }
@@ -1001,7 +1038,7 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
         return RECUR_ESIZE;
     if ((rc = check({strided(cfg, in->x, in->ldx, T), strided(cfg, in->r, in->ldr, T), strided(cfg, in->i, in->ldi, T),
                      states_of(cfg, lam, 1, true), Buf{Span{offsets, offsets ? 4 * ((uint64_t)n + 1) : 0}, 4, false},
-                     states_of(cfg, h0, n), states_of(cfg, saved, chunks(T), true), rows_of(cfg, dy, T),
+                     states_of(cfg, h0, n), states_of(cfg, saved, saved_rows(T), true), rows_of(cfg, dy, T),
                      states_of(cfg, dhT, n)},
                     {strided(cfg, out->dx, out->lddx, T), strided(cfg, out->dr, out->lddr, T),
                      strided(cfg, out->di, out->lddi, T), states_of(cfg, dlam, 1, true), states_of(cfg, dh0, n)},
@@ -1023,22 +1060,20 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     a.lddi = out->lddi * e;
     a.dlam = dlam;
     a.dh0 = dh0;
-    if (n == 0) {   // no sequence: nothing but dlam
-        a.chunks = 0;
-        T = 0;
-    }
+    if (n == 0)   // no sequence: nothing but dlam
+        a.T = T = 0;
     if (T == 0 && a.accum && !dh0)
         return RECUR_OK;
-    place_words(a, ws);
+    place_words(a, RECUR_PASS_BWD, ws);
     hipStream_t s = (hipStream_t)stream;
     clear(a, dhT, dh0, s);
     if (T) {
         const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
         auto k = f32 ? (one ? bwd_kernel<4, 1> : bwd_kernel<4, 2>) : (one ? bwd_kernel<2, 1> : bwd_kernel<2, 2>);
-        k<<<(unsigned)(a.chunks * (int64_t)a.columns), kThreads, 0, s>>>(a);
+        k<<<(unsigned)(chunks(RECUR_PASS_BWD, T) * a.columns), kBwdWaves * 64, 0, s>>>(a);
     }
     if (T || !a.accum)
-        dlam_kernel<<<(cfg->dim + 63) / 64, 1024, 0, s>>>(a);
+        dlam_kernel<<<(cfg->dim + 15) / 16, 1024, 0, s>>>(a);
     return done();
 }
 

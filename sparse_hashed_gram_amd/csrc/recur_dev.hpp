@@ -10,10 +10,11 @@
 
 namespace recur {
 
-constexpr int kChunk = RECUR_CHUNK;   // positions of a block
-constexpr int kWaves = 8;             // wavefronts of a block
-constexpr int kSteps = kChunk / kWaves;
-constexpr int kGroup = 32;            // chunks between two states that are passed on
+// A block takes a chunk of WAVES * STEPS positions, STEPS to a wavefront.
+constexpr int kFwdWaves = 4, kFwdSteps = 16, kFwdChunk = kFwdWaves * kFwdSteps;
+constexpr int kBwdWaves = 4, kBwdSteps = 8, kBwdChunk = kBwdWaves * kBwdSteps;
+static_assert(kBwdChunk == RECUR_CHUNK, "a saved state in front of every backward chunk");
+constexpr int kGroup = 16;   // chunks between two states that are passed on
 
 struct Args {
     const uint8_t *x, *r, *i, *dy;
@@ -24,7 +25,8 @@ struct Args {
     int64_t lddx, lddr, lddi;   // bytes
     float *hT, *saved, *dlam, *dh0;
     int64_t T, n;
-    int D, accum, chunks, columns;   // columns: blocks side by side
+    int D, accum, columns;   // columns: blocks side by side
+    bool alone;              // one chunk: nobody waits
     float c;
     // workspace
     uint32_t *ticket;

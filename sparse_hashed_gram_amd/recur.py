@@ -28,7 +28,7 @@ _TORCH = (torch.float32, torch.bfloat16)
 OPT_ACCUM = 0x1
 PASS_FWD = 0
 PASS_BWD = 1
-CHUNK = 64
+CHUNK = 32
 
 
 class RecurConfig(ctypes.Structure):

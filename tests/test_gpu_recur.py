@@ -491,13 +491,10 @@ def test_rows_past_32_bits():
     assert (y[:1000] == 0).all() and (y[-1100:-100] == 0).all()
     dy = x
     g = m.bwd(cfg, ws, x, r, i, lam, saved, dy, off)
-    tail = [v[-164:].contiguous() for v in (x, r, i)]   # as far from a piece's start as there
-    off2 = torch.tensor([0, 64, 164], dtype=torch.int32, device="cuda")
-    shift = (T - 164) % 64
-    pad = [torch.cat([torch.zeros(shift, D, dtype=v.dtype, device="cuda"), v]) for v in tail]
-    off2 = off2 + shift
-    y2, _, s2 = m.fwd(cfg, ws, *pad, lam, off2, keep=True)
-    g2 = m.bwd(cfg, ws, *pad, lam, s2, pad[0], off2)
-    assert torch.equal(y[-100:], y2[-100:])
-    for k in ("dx", "dr", "di"):
-        assert torch.equal(g[k][-100:], g2[k][-100:]), k
+    tail = [v[-100:].contiguous() for v in (x, r, i)]
+    y2, _, s2 = m.fwd(cfg, ws, *tail, lam, keep=True)
+    g2 = m.bwd(cfg, ws, *tail, lam, s2, tail[0])
+    # two roundings to bf16 of values that differ by fp32 sums' errors: a step apart at most
+    for p, q in ((y, y2), *((g[k], g2[k]) for k in ("dx", "dr", "di"))):
+        p, q = p[-100:].double(), q.double()
+        assert (q.abs().sum(1) > 0).all() and ((p - q).abs() <= 2.0 ** -7 * q.abs() + 1e-5 * q.abs().max()).all()

@@ -53,11 +53,11 @@ def test_config_rejects(M, field, value):
 def test_sizes(M):
     c = M.config(768, 49152)
     f, b = M.workspace_bytes(c, False), M.workspace_bytes(c)
-    assert 0 < f <= b <= 768 * 49152 * 0.2 + (1 << 16)
+    assert 0 < f <= b <= 768 * 49152 * 0.34 + (1 << 16)
     n, L = ctypes.c_uint64(), M.lib()
     assert L.recur_workspace_bytes(c, 2, ctypes.byref(n)) == -5 and L.recur_workspace_bytes(c, 0, None) == -1
-    for T, rows in ((0, 0), (1, 1), (64, 1), (65, 2), (49152, 768)):
-        assert L.recur_saved_bytes(c, T, ctypes.byref(n)) == 0 and n.value == rows * 768 * 4
+    for T in (0, 1, M.CHUNK, M.CHUNK + 1, 49152):
+        assert L.recur_saved_bytes(c, T, ctypes.byref(n)) == 0 and n.value == -(-T // M.CHUNK) * 768 * 4
     assert L.recur_saved_bytes(c, 49153, ctypes.byref(n)) == -4 and L.recur_saved_bytes(c, -1, ctypes.byref(n)) == -4
     assert L.recur_saved_bytes(c, 1, None) == -1
 
@@ -122,17 +122,6 @@ def test_backward_refusals(M):
     assert call(dx=A[9], dr=A[9] + 63 * e, di=A[9] + 128 * e, lddx=192, lddr=192, lddi=192) == -5
     assert call(dx=A[9], dr=A[9] + 64 * e, di=A[9] + 129 * e, lddx=192, lddr=192, lddi=192) == -5   # wraps onto dx's next row
     assert call(dx=A[9], dr=A[9] + 64 * e, di=A[11], lddx=192, lddr=200, lddi=192) == -5             # rows drift apart
-
-
-def test_too_many_pieces(M):
-    # T and D in their ranges, but over 2^23 - 1 blocks
-    c = M.config(16384, 1 << 24)
-    n = M.workspace_bytes(c)
-    i = M.RecurInputs(1 << 50, 1 << 51, 1 << 52, 16384, 16384, 16384)
-    assert M.lib().recur_fwd(c, 1 << 53, n, i, A[0], None, 1, None, 1 << 24, 1 << 54, None, None, None) == -4
-    g = M.RecurGrads(1 << 55, 1 << 56, 1 << 57, 16384, 16384, 16384)
-    assert M.lib().recur_bwd(c, 1 << 53, n, i, A[0], None, 1, None, 1 << 58, 1 << 54, None, 1 << 24, g, A[1], None,
-                             None) == -4
 
 
 def test_step_refusals(M):
