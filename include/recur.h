@@ -63,7 +63,7 @@ extern "C" {
 #define RECUR_ESIZE -4   /* T outside [0, max_tokens], n outside [0, 2^24] (1
                             without offsets), a distance between rows under D or
                             over 2^31 - 1, a workspace too small, or 2^23 and
-                            more pieces of 48 positions by 128 (D up to 64: 64)
+                            more pieces of 32 positions by 128 (D up to 64: 64)
                             channels                                           */
 #define RECUR_EARG -5    /* an output that overlaps an operand or another output,
                             or an unknown pass                                 */
@@ -113,7 +113,7 @@ const char *recur_status_string(int status);
 int recur_config_check(const recur_config *cfg);
 
 /* Bytes of workspace that a pass of cfg needs (host output `bytes`); one of the
- * backward's size serves both.  About D max_tokens / 3 bytes. */
+ * backward's size serves both.  About 2 / 5 D max_tokens bytes (forward: 1 / 7). */
 int recur_workspace_bytes(const recur_config *cfg, int pass, uint64_t *bytes);
 
 /* Bytes of `saved` for T positions: 4 D ceil(T / RECUR_CHUNK). */

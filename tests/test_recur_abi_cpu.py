@@ -53,7 +53,7 @@ def test_config_rejects(M, field, value):
 def test_sizes(M):
     c = M.config(768, 49152)
     f, b = M.workspace_bytes(c, False), M.workspace_bytes(c)
-    assert 0 < f <= b <= 768 * 49152 * 0.34 + (1 << 16)
+    assert 0 < f <= b <= 768 * 49152 * 0.41 + (1 << 16)
     n, L = ctypes.c_uint64(), M.lib()
     assert L.recur_workspace_bytes(c, 2, ctypes.byref(n)) == -5 and L.recur_workspace_bytes(c, 0, None) == -1
     for T in (0, 1, M.CHUNK, M.CHUNK + 1, 49152):
