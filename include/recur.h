@@ -63,8 +63,8 @@ extern "C" {
 #define RECUR_ESIZE -4   /* T outside [0, max_tokens], n outside [0, 2^24] (1
                             without offsets), a distance between rows under D or
                             over 2^31 - 1, a workspace too small, or 2^23 and
-                            more pieces of 32 positions by 128 (D up to 64: 64)
-                            channels                                           */
+                            more blocks: pieces of 32 (forward: 64) positions by
+                            128 (D up to 64: 64) channels                      */
 #define RECUR_EARG -5    /* an output that overlaps an operand or another output,
                             or an unknown pass                                 */
 #define RECUR_EHIP -6    /* the HIP runtime reported an error                  */

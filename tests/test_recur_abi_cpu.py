@@ -124,6 +124,17 @@ def test_backward_refusals(M):
     assert call(dx=A[9], dr=A[9] + 64 * e, di=A[11], lddx=192, lddr=200, lddi=192) == -5             # rows drift apart
 
 
+def test_too_many_pieces(M):
+    # T and D in their ranges, but over 2^23 - 1 blocks
+    c = M.config(16384, 1 << 24)
+    n = M.workspace_bytes(c)
+    i = M.RecurInputs(1 << 50, 1 << 51, 1 << 52, 16384, 16384, 16384)
+    assert M.lib().recur_fwd(c, 1 << 53, n, i, A[0], None, 1, None, 1 << 24, 1 << 54, None, None, None) == -4
+    g = M.RecurGrads(1 << 55, 1 << 56, 1 << 57, 16384, 16384, 16384)
+    assert M.lib().recur_bwd(c, 1 << 53, n, i, A[0], None, 1, None, 1 << 58, 1 << 54, None, 1 << 24, g, A[1], None,
+                             None) == -4
+
+
 def test_step_refusals(M):
     L, c = M.lib(), M.config(64, 100)
 
