@@ -47,7 +47,7 @@ __device__ __forceinline__ float param_at(const uint8_t *p, int f32, int one, in
 // a column.  blockIdx.y: the norm in front, the norm and gate behind, the scale.
 __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
 {
-    __shared__ float lds[2][64][16];
+    __shared__ float lds[2][16][16];
     const int c = threadIdx.x % 16, g = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     const int ld = (a.D + 3) / 4 * 4, what = blockIdx.y;
     const int first = what == 0 ? kSumPreW : what == 1 ? kSumPost1 : kSumScale;
@@ -63,13 +63,19 @@ __global__ __launch_bounds__(1024) void grad_kernel(GradArgs a)
             y += p[apart];
         }
     }
-    lds[0][g][c] = x;
-    lds[1][g][c] = y;
+    x += __shfl_xor(x, 16);
+    y += __shfl_xor(y, 16);
+    x += __shfl_xor(x, 32);
+    y += __shfl_xor(y, 32);
+    if (g % 4 == 0) {
+        lds[0][g / 4][c] = x;
+        lds[1][g / 4][c] = y;
+    }
     __syncthreads();
     if (g != 0 || j >= a.D)
         return;
 #pragma unroll
-    for (int i = 1; i < 64; ++i) {
+    for (int i = 1; i < 16; ++i) {
         x += lds[0][i][c];
         y += lds[1][i][c];
     }

@@ -32,10 +32,36 @@ struct Bits {
     uint32_t starts, ends, inside;
 };
 
-// All threads of the block.  The sequences that can matter: those from the last
-// probe that begins in front of t0 to the first that begins behind the chunk.
+// Barrier that waits for LDS accesses only: a fence would wait for the rows' loads,
+// which are on their way.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A sequence's first row and the one behind its last; read before the chunk's rows are
+// asked for, because loads come back in order.
+struct Ends {
+    int32_t begin = 0, end = 0;
+
+    __device__ __forceinline__ void load(const Args &a, int64_t s)
+    {
+        begin = end = 0;
+        if (a.offsets && s < a.n) {
+            begin = a.offsets[s];
+            end = a.offsets[s + 1];
+        }
+    }
+};
+
+// All threads of the block; mine: the sequence of the thread's own number.  The
+// sequences that can matter, where there are many: those from the last probe that
+// begins in front of t0 to the first that begins behind the chunk.
 template <int WAVES, int STEPS>
-__device__ void find_marks(const Args &a, int64_t t0, Marks<WAVES, STEPS> *m)
+__device__ __forceinline__ void find_marks(const Args &a, int64_t t0, Ends mine, Marks<WAVES, STEPS> *m)
 {
     constexpr int threads = WAVES * 64, N = WAVES * STEPS;
     __shared__ int from, to;
@@ -45,22 +71,11 @@ __device__ void find_marks(const Args &a, int64_t t0, Marks<WAVES, STEPS> *m)
         from = 0;
         to = (int)a.n;
     }
-    __syncthreads();
-    if (a.n > 4 * threads) {
-        const int64_t step = (a.n + threads - 1) / threads, at = threadIdx.x * step;
-        if (at < a.n) {
-            const int32_t v = a.offsets[at];
-            if (v < t0)
-                atomicMax(&from, (int)at);
-            if (v > t0 + N)
-                atomicMin(&to, (int)at);
-        }
-        __syncthreads();
-    }
-    for (int s = from + (int)threadIdx.x; s < to; s += threads) {
-        const int64_t b = a.offsets[s] - t0, e = a.offsets[s + 1] - t0 - 1;   // first and last position
+    lds_barrier();
+    auto mark = [&](int s, const Ends &k) {
+        const int64_t b = (int64_t)k.begin - t0, e = (int64_t)k.end - t0 - 1;   // first and last position
         if (b > e)
-            continue;
+            return;
         if (b >= 0 && b < N) {
             atomicOr(&m->starts[b / STEPS], 1u << (b % STEPS));
             m->start_of[b / STEPS][b % STEPS] = s;
@@ -69,8 +84,29 @@ __device__ void find_marks(const Args &a, int64_t t0, Marks<WAVES, STEPS> *m)
             atomicOr(&m->ends[e / STEPS], 1u << (e % STEPS));
             m->end_of[e / STEPS][e % STEPS] = s;
         }
+    };
+    if (a.n <= 4 * threads) {
+        mark((int)threadIdx.x, mine);
+        for (int s = threads + (int)threadIdx.x; s < a.n; s += threads) {
+            mine.load(a, s);
+            mark(s, mine);
+        }
+    } else {
+        const int64_t step = (a.n + threads - 1) / threads, at = threadIdx.x * step;
+        if (at < a.n) {
+            const int32_t v = a.offsets[at];
+            if (v < t0)
+                atomicMax(&from, (int)at);
+            if (v > t0 + N)
+                atomicMin(&to, (int)at);
+        }
+        lds_barrier();
+        for (int s = from + (int)threadIdx.x; s < to; s += threads) {
+            mine.load(a, s);
+            mark(s, mine);
+        }
     }
-    __syncthreads();
+    lds_barrier();
 }
 
 // The block's chunk, and its place side by side.  A block that waits for others
@@ -222,21 +258,24 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STE
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 s[v] = join(s[v], sh.before[i][v][lane]);
-        if (group > 0 || place == kGroup - 1) {
-            if (wave == WAVES - 1) {
+        // where a sequence began in between (the same for all channels), nothing in front counts
+        const bool cut = __all(s[0].A < 0.0f);
+        if (wave == WAVES - 1) {
+            if (asks && !cut)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    h[v] = asks ? span(wait_for(q + v * 64, first[v])).H : 0.0f;
-                if (place == kGroup - 1 && index + 1 < chunks) {
+                    h[v] = span(wait_for(q + v * 64, first[v])).H;
+            if (place == kGroup - 1 && index + 1 < chunks)
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        publish(a.states + (group + 1) * step + at + v * 64,
-                                word(Span1{1.0f, through(sh.all[v][lane], through(s[v], h[v]))}));
-                }
+                for (int v = 0; v < V; ++v)
+                    publish(a.states + (group + 1) * step + at + v * 64,
+                            word(Span1{1.0f, through(sh.all[v][lane], through(s[v], h[v]))}));
+        }
+        if (group > 0 && !cut) {
+            if (wave == WAVES - 1)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     sh.state[v][lane] = h[v];
-            }
             __syncthreads();
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -335,6 +374,9 @@ __global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Arg
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;   // behind a row's address, which is the same for all lanes
     const int64_t t0 = (int64_t)chunk * kFwdChunk, t = t0 + wave * STEPS;
+    Ends mine;
+    mine.load(a, threadIdx.x);
+    __builtin_amdgcn_sched_barrier(0);
     Raw<E, V> x[STEPS], r[STEPS], i[STEPS];
     load_rows<E, V, STEPS>(a.r, a.ldr, t, a.T, off, r);
     load_rows<E, V, STEPS>(a.i, a.ldi, t, a.T, off, i);
@@ -348,7 +390,7 @@ __global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Arg
     if (t0 >= hi)
         return;   // nor does any chunk behind it ask
     if (a.offsets)
-        find_marks<WAVES, STEPS>(a, t0, &sh.marks);
+        find_marks<WAVES, STEPS>(a, t0, mine, &sh.marks);
     const Bits bits = bits_of<WAVES, STEPS>(a, sh.marks, t, lo, hi, wave);
     const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << STEPS) - 1;
     float av[STEPS][V], u[STEPS][V];
@@ -514,6 +556,9 @@ __global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Arg
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;
     const int64_t t0 = (int64_t)chunk * kBwdChunk, t = t0 + wave * STEPS;
+    Ends mine;
+    mine.load(a, threadIdx.x);
+    __builtin_amdgcn_sched_barrier(0);
     Raw<E, V> x[STEPS], r[STEPS], i[STEPS], d[STEPS];
     load_rows<E, V, STEPS>(a.r, a.ldr, t, a.T, off, r);
     load_rows<E, V, STEPS>(a.i, a.ldi, t, a.T, off, i);
@@ -526,7 +571,7 @@ __global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Arg
         h[v] = a.saved[(int64_t)chunk * a.D + j + v];
     }
     if (a.offsets)
-        find_marks<WAVES, STEPS>(a, t0, &sh.marks);
+        find_marks<WAVES, STEPS>(a, t0, mine, &sh.marks);
     const Bits bits = bits_of<WAVES, STEPS>(a, sh.marks, t, lo, hi, wave);
     const bool plain = bits.starts == 0 && bits.ends == 0 && bits.inside == (1u << STEPS) - 1;
     float av[STEPS][V], c1[STEPS][V], c2[STEPS][V], c3[STEPS][V], cr[STEPS][V], cl[STEPS][V];
@@ -701,7 +746,7 @@ __global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Arg
 // a channel.
 __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 {
-    __shared__ float lds[64][16];
+    __shared__ float lds[16][16];
     const int c = threadIdx.x % 16, g = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     float s = 0.0f;
     if (j < a.D && a.T > 0) {
@@ -712,12 +757,15 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
         for (int64_t k = g; k < chunks; k += 64)
             s += a.part[k * a.D + j];
     }
-    lds[g][c] = s;
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (g % 4 == 0)
+        lds[g / 4][c] = s;
     __syncthreads();
     if (g != 0 || j >= a.D)
         return;
 #pragma unroll
-    for (int k = 1; k < 64; ++k)
+    for (int k = 1; k < 16; ++k)
         s += lds[k][c];
     const float v = alone(-a.c * sigmoid(a.lam[j]), s);
     a.dlam[j] = a.accum ? a.dlam[j] + v : v;
@@ -819,14 +867,17 @@ int64_t chunks(int pass, int64_t T)
 }
 uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-// A lane takes two channels; up to 64 channels one, or half the wavefront would
-// have none.
-int per_lane(int D) { return D <= 64 ? 1 : 2; }
-int64_t columns(int D) { return (D + 64 * per_lane(D) - 1) / (64 * per_lane(D)); }
+// Channels of a lane: two, but one up to 64 channels, where half the wavefront would
+// have none, and for few rows of chunks (or a step's rows).
+constexpr int64_t kFewBlocks = 64;
+int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <= kFewBlocks ? 1 : 2; }
+int64_t columns(int D, int per) { return (D + 64 * per - 1) / (64 * per); }
 
 // Workspace: the ticket, the words of n chunks and their groups, the backward's
 // parts of dlam.
-uint64_t words_of(int D, int64_t n) { return (uint64_t)(n + n / kGroup + 1) * columns(D) * per_lane(D) * 64; }
+// Words of a row of chunks: enough for one or two channels a lane.
+uint64_t row_words(int D) { return (uint64_t)columns(D, 2) * 128; }
+uint64_t words_of(int D, int64_t n) { return (uint64_t)(n + n / kGroup + 1) * row_words(D); }
 uint64_t ws_need(const recur_config *c, int pass)
 {
     const int64_t n = chunks(pass, c->max_tokens);
@@ -894,7 +945,7 @@ int check_call(const recur_config *cfg, int pass, const void *ws, uint64_t ws_by
         return RECUR_EALIGN;
     if (T < 0 || T > cfg->max_tokens || n < 0 || n > (int64_t(1) << 24) || (!offsets && n != 1) ||
         bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi) || ws_bytes < ws_need(cfg, pass) ||
-        chunks(pass, T) * columns(cfg->dim) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
+        chunks(pass, T) * columns(cfg->dim, 2) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
         return RECUR_ESIZE;
     return RECUR_OK;
 }
@@ -914,7 +965,6 @@ Args base(const recur_config *c, const recur_inputs *in, const float *lam, int64
     a.D = c->dim;
     a.c = c->c;
     a.accum = (c->options & RECUR_OPT_ACCUM) != 0;
-    a.columns = (int)columns(c->dim);
     return a;
 }
 
@@ -922,11 +972,13 @@ void place_words(Args &a, int pass, void *ws)
 {
     uint8_t *p = (uint8_t *)ws;
     const int64_t n = chunks(pass, a.T);
+    a.per = per_lane(a.D, n);
+    a.columns = (int)columns(a.D, a.per);
     a.alone = n <= 1;
     a.words = (int64_t)words_of(a.D, n);
     a.ticket = (uint32_t *)p;
     a.sums = (uint64_t *)(p + kAlign);
-    a.states = a.sums + n * a.columns * per_lane(a.D) * 64;
+    a.states = a.sums + n * (int64_t)row_words(a.D);
     a.part = (float *)(p + kAlign + align_up((uint64_t)a.words * 8));
 }
 
@@ -1018,7 +1070,7 @@ int recur_fwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     hipStream_t s = (hipStream_t)stream;
     clear(a, h0, hT, s);
     if (T) {
-        const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
+        const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = a.per == 1;
         auto k = f32 ? (one ? fwd_kernel<4, 1> : fwd_kernel<4, 2>) : (one ? fwd_kernel<2, 1> : fwd_kernel<2, 2>);
         k<<<(unsigned)(chunks(RECUR_PASS_FWD, T) * a.columns), kFwdWaves * 64, 0, s>>>(a);
     }
@@ -1068,7 +1120,7 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     hipStream_t s = (hipStream_t)stream;
     clear(a, dhT, dh0, s);
     if (T) {
-        const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
+        const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = a.per == 1;
         auto k = f32 ? (one ? bwd_kernel<4, 1> : bwd_kernel<4, 2>) : (one ? bwd_kernel<2, 1> : bwd_kernel<2, 2>);
         k<<<(unsigned)(chunks(RECUR_PASS_BWD, T) * a.columns), kBwdWaves * 64, 0, s>>>(a);
     }
@@ -1097,7 +1149,10 @@ int recur_step(const recur_config *cfg, const recur_inputs *in, const float *lam
     Args a = base(cfg, in, lam, n);
     a.y = (uint8_t *)y;
     a.n = n;
-    const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = per_lane(cfg->dim) == 1;
+    const bool f32 = cfg->dtype == RECUR_DTYPE_F32;
+    a.per = per_lane(a.D, n);
+    a.columns = (int)columns(a.D, a.per);
+    const bool one = a.per == 1;
     auto k = f32 ? (one ? step_kernel<4, 1> : step_kernel<4, 2>) : (one ? step_kernel<2, 1> : step_kernel<2, 2>);
     k<<<(unsigned)((n * a.columns + 3) / 4), 256, 0, (hipStream_t)stream>>>(a, state, (int)states, slots, (int)n);
     return done();

@@ -25,7 +25,7 @@ struct Args {
     int64_t lddx, lddr, lddi;   // bytes
     float *hT, *saved, *dlam, *dh0;
     int64_t T, n;
-    int D, accum, columns;   // columns: blocks side by side
+    int D, accum, per, columns;   // channels of a lane; columns: blocks side by side
     bool alone;              // one chunk: nobody waits
     float c;
     // workspace
