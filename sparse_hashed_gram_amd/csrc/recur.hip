@@ -193,7 +193,7 @@ __device__ __forceinline__ uint64_t wait_for(const uint64_t *p, uint64_t w)
 }
 
 template <int V, int WAVES, int STEPS>
-__device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STEPS> &sh, int chunks, int index, int column,
+__device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STEPS> &sh, int index, int column,
                                              int wave, int order, int lane, const Span1 (&own)[V], float (&h)[V])
 {
 #pragma unroll
@@ -203,7 +203,7 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STE
 #pragma unroll
     for (int v = 0; v < V; ++v)
         h[v] = 0.0f;
-    if (chunks <= 1)
+    if (a.alone)
         return;
     constexpr int per = (kGroup + WAVES - 1) / WAVES;
     const int group = index / kGroup, place = index % kGroup;
@@ -265,7 +265,7 @@ __device__ __forceinline__ void state_before(const Args &a, Shared<V, WAVES, STE
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     h[v] = span(wait_for(q + v * 64, first[v])).H;
-            if (place == kGroup - 1 && index + 1 < chunks)
+            if (place == kGroup - 1 && index + 1 < a.chunks)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     publish(a.states + (group + 1) * step + at + v * 64,
@@ -362,10 +362,10 @@ __device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kFwdSteps], const
     }
 }
 
-template <int E, int V>
-__global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Args a)
+template <int E, int V, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void fwd_kernel(Args a)
 {
-    constexpr int WAVES = kFwdWaves, STEPS = kFwdSteps;
+    constexpr int STEPS = kFwdSteps, N = WAVES * STEPS;
     __shared__ Shared<V, WAVES, STEPS> sh;
     int chunk, column;
     place(a, chunk, column);
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Arg
     // lanes past the last channels take those again: the same loads, values and stores
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;   // behind a row's address, which is the same for all lanes
-    const int64_t t0 = (int64_t)chunk * kFwdChunk, t = t0 + wave * STEPS;
+    const int64_t t0 = (int64_t)chunk * N, t = t0 + wave * STEPS;
     Ends mine;
     mine.load(a, threadIdx.x);
     __builtin_amdgcn_sched_barrier(0);
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(kFwdWaves * 64, E == 2 ? 3 : 2) void fwd_kernel(Arg
         }
     }
     float h[V];
-    state_before<V, WAVES, STEPS>(a, sh, (int)((hi + kFwdChunk - 1) / kFwdChunk), chunk, column, wave, wave, lane, own, h);
+    state_before<V, WAVES, STEPS>(a, sh, chunk, column, wave, wave, lane, own, h);
     for (int w = 0; w < wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -500,6 +500,13 @@ __device__ __forceinline__ void row_of(const float *p, int64_t sequence, int D, 
         to[v].H = p ? p[sequence * D + j + v] : 0.0f;
 }
 
+// A channel's dlam from its sum of rho dz.
+__device__ __forceinline__ void put_dlam(const Args &a, int j, float sum)
+{
+    const float v = alone(-a.c * sigmoid(a.lam[j]), sum);
+    a.dlam[j] = a.accum ? a.dlam[j] + v : v;
+}
+
 // A position's numbers that need no state: a, m g (dx / G), m g x (1 - g) (di / G), and
 // of dz / G the part beside a h_{t-1}: g x a^2 / m.
 template <int E, int V, bool ALL>
@@ -527,12 +534,14 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const
             cr[k][v] = z * rho_rest;
             // where m is 0, z is too, and with it what this is multiplied by
             c3[k][v] = g * xf[v] * (av[k][v] * av[k][v] * __builtin_amdgcn_rcpf(fmaxf(m, 1e-18f)));
+            here(av[k][v]);
             here(c1[k][v]);
             here(c2[k][v]);
             here(c3[k][v]);
             here(cl[k][v]);
             here(cr[k][v]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -540,22 +549,20 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const
 // through the chunk; with them and the gates every output is G_t times a number of
 // its position: dx c1, di c2, dr cr, and rho dz (of dlam) cl.  G in turn runs
 // backwards, what a position hands on being a_t G_t.
-template <int E, int V>
-__global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Args a)
+template <int E, int V, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void bwd_kernel(Args a)
 {
-    constexpr int WAVES = kBwdWaves, STEPS = kBwdSteps;
+    constexpr int STEPS = kBwdSteps, N = WAVES * STEPS;
     __shared__ Shared<V, WAVES, STEPS> sh;
     int index, column;
     place(a, index, column);
     int64_t lo, hi;
     rows_of_sequences(a, lo, hi);
-    const int chunks = (int)((hi + kBwdChunk - 1) / kBwdChunk), chunk = chunks - 1 - index;
-    if (chunk < 0)
-        return;   // behind the last sequence: as many blocks as chunks are left
+    const int chunk = a.chunks - 1 - index;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int j = min((column * 64 + lane) * V, a.D - V);
     const uint32_t off = (uint32_t)j * E;
-    const int64_t t0 = (int64_t)chunk * kBwdChunk, t = t0 + wave * STEPS;
+    const int64_t t0 = (int64_t)chunk * N, t = t0 + wave * STEPS;
     Ends mine;
     mine.load(a, threadIdx.x);
     __builtin_amdgcn_sched_barrier(0);
@@ -678,7 +685,7 @@ __global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Arg
         }
     }
     float in[V], acc[V];
-    state_before<V, WAVES, STEPS>(a, sh, chunks, index, column, wave, WAVES - 1 - wave, lane, back, in);
+    state_before<V, WAVES, STEPS>(a, sh, index, column, wave, WAVES - 1 - wave, lane, back, in);
     for (int w = 0; w < WAVES - 1 - wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v)
@@ -737,7 +744,10 @@ __global__ __launch_bounds__(kBwdWaves * 64, E == 2 ? 3 : 2) void bwd_kernel(Arg
 #pragma unroll
             for (int w = 1; w < WAVES; ++w)
                 s += sh.waves[w][v][lane].A;
-            a.part[(int64_t)chunk * a.D + j + v] = s;
+            if (V == 1 && a.alone)   // the only chunk: one channel a lane
+                put_dlam(a, j + v, s);
+            else
+                a.part[(int64_t)chunk * a.D + j + v] = s;
         }
     }
 }
@@ -749,12 +759,9 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
     __shared__ float lds[16][16];
     const int c = threadIdx.x % 16, g = threadIdx.x / 16, j = blockIdx.x * 16 + c;
     float s = 0.0f;
-    if (j < a.D && a.T > 0) {
-        int64_t lo, hi;
-        rows_of_sequences(a, lo, hi);
-        const int64_t chunks = (hi + kBwdChunk - 1) / kBwdChunk;
+    if (j < a.D) {
 #pragma unroll 16
-        for (int64_t k = g; k < chunks; k += 64)
+        for (int64_t k = g; k < a.chunks; k += 64)
             s += a.part[k * a.D + j];
     }
     s += __shfl_xor(s, 16);
@@ -767,8 +774,7 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 #pragma unroll
     for (int k = 1; k < 16; ++k)
         s += lds[k][c];
-    const float v = alone(-a.c * sigmoid(a.lam[j]), s);
-    a.dlam[j] = a.accum ? a.dlam[j] + v : v;
+    put_dlam(a, j, s);
 }
 
 // The rows of one slot: whether `row` is the first of them (it takes them all, in
@@ -860,11 +866,15 @@ int check_config(const recur_config *c)
 }
 
 int64_t saved_rows(int64_t T) { return (T + RECUR_CHUNK - 1) / RECUR_CHUNK; }
-int64_t chunks(int pass, int64_t T)
+// Wavefronts of a block: the usual ones, or many where a call that they have not room
+// for is then one chunk, with no words to clear and nobody to wait for.
+int waves(int pass, int64_t T)
 {
-    const int n = pass == RECUR_PASS_FWD ? kFwdChunk : kBwdChunk;
-    return (T + n - 1) / n;
+    const int steps = pass == RECUR_PASS_FWD ? kFwdSteps : kBwdSteps;
+    return T > kWaves * steps && T <= kManyWaves * steps ? kManyWaves : kWaves;
 }
+int64_t chunk_of(int pass, int64_t T) { return waves(pass, T) * (pass == RECUR_PASS_FWD ? kFwdSteps : kBwdSteps); }
+int64_t chunks(int pass, int64_t T) { return (T + chunk_of(pass, T) - 1) / chunk_of(pass, T); }
 uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // Channels of a lane: two, but one up to 64 channels, where half the wavefront would
@@ -972,8 +982,9 @@ void place_words(Args &a, int pass, void *ws)
 {
     uint8_t *p = (uint8_t *)ws;
     const int64_t n = chunks(pass, a.T);
-    a.per = per_lane(a.D, n);
+    a.per = n <= 1 ? 1 : per_lane(a.D, n);   // 1,024 threads have 128 registers
     a.columns = (int)columns(a.D, a.per);
+    a.chunks = (int)n;
     a.alone = n <= 1;
     a.words = (int64_t)words_of(a.D, n);
     a.ticket = (uint32_t *)p;
@@ -1071,8 +1082,11 @@ int recur_fwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     clear(a, h0, hT, s);
     if (T) {
         const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = a.per == 1;
-        auto k = f32 ? (one ? fwd_kernel<4, 1> : fwd_kernel<4, 2>) : (one ? fwd_kernel<2, 1> : fwd_kernel<2, 2>);
-        k<<<(unsigned)(chunks(RECUR_PASS_FWD, T) * a.columns), kFwdWaves * 64, 0, s>>>(a);
+        const int w = waves(RECUR_PASS_FWD, T);
+        auto k = w == kManyWaves ? (f32 ? fwd_kernel<4, 1, kManyWaves> : fwd_kernel<2, 1, kManyWaves>)
+                 : f32           ? (one ? fwd_kernel<4, 1, kWaves> : fwd_kernel<4, 2, kWaves>)
+                                 : (one ? fwd_kernel<2, 1, kWaves> : fwd_kernel<2, 2, kWaves>);
+        k<<<(unsigned)(chunks(RECUR_PASS_FWD, T) * a.columns), w * 64, 0, s>>>(a);
     }
     return done();
 }
@@ -1121,10 +1135,13 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     clear(a, dhT, dh0, s);
     if (T) {
         const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = a.per == 1;
-        auto k = f32 ? (one ? bwd_kernel<4, 1> : bwd_kernel<4, 2>) : (one ? bwd_kernel<2, 1> : bwd_kernel<2, 2>);
-        k<<<(unsigned)(chunks(RECUR_PASS_BWD, T) * a.columns), kBwdWaves * 64, 0, s>>>(a);
+        const int w = waves(RECUR_PASS_BWD, T);
+        auto k = w == kManyWaves ? (f32 ? bwd_kernel<4, 1, kManyWaves> : bwd_kernel<2, 1, kManyWaves>)
+                 : f32           ? (one ? bwd_kernel<4, 1, kWaves> : bwd_kernel<4, 2, kWaves>)
+                                 : (one ? bwd_kernel<2, 1, kWaves> : bwd_kernel<2, 2, kWaves>);
+        k<<<(unsigned)(chunks(RECUR_PASS_BWD, T) * a.columns), w * 64, 0, s>>>(a);
     }
-    if (T || !a.accum)
+    if (T ? !a.alone : !a.accum)
         dlam_kernel<<<(cfg->dim + 15) / 16, 1024, 0, s>>>(a);
     return done();
 }

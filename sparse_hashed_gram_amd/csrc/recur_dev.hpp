@@ -11,9 +11,9 @@
 namespace recur {
 
 // A block takes a chunk of WAVES * STEPS positions, STEPS to a wavefront.
-constexpr int kFwdWaves = 4, kFwdSteps = 16, kFwdChunk = kFwdWaves * kFwdSteps;
-constexpr int kBwdWaves = 4, kBwdSteps = 8, kBwdChunk = kBwdWaves * kBwdSteps;
-static_assert(kBwdChunk == RECUR_CHUNK, "a saved state in front of every backward chunk");
+constexpr int kWaves = 4, kFwdSteps = 16, kBwdSteps = 8;
+constexpr int kManyWaves = 16;   // where that makes one chunk of the whole call
+static_assert(kWaves * kBwdSteps == RECUR_CHUNK, "a saved state in front of every backward chunk");
 constexpr int kGroup = 16;   // chunks between two states that are passed on
 
 struct Args {
@@ -26,6 +26,7 @@ struct Args {
     float *hT, *saved, *dlam, *dh0;
     int64_t T, n;
     int D, accum, per, columns;   // channels of a lane; columns: blocks side by side
+    int chunks;              // in a column
     bool alone;              // one chunk: nobody waits
     float c;
     // workspace
