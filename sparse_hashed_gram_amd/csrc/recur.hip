@@ -744,10 +744,12 @@ __global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void
 #pragma unroll
             for (int w = 1; w < WAVES; ++w)
                 s += sh.waves[w][v][lane].A;
-            if (V == 1 && a.alone)   // the only chunk: one channel a lane
-                put_dlam(a, j + v, s);
-            else
+            if (V == 1 && a.alone) {   // the only chunk: one channel a lane
+                if (column * 64 + lane < a.D)   // it may add to what is there: once
+                    put_dlam(a, j, s);
+            } else {
                 a.part[(int64_t)chunk * a.D + j + v] = s;
+            }
         }
     }
 }
@@ -793,7 +795,8 @@ __device__ __forceinline__ bool first_of_slot(const int32_t *slots, int n, int r
     return !__any(before);
 }
 
-// A wavefront takes a row and V channels a lane.
+// A wavefront takes a row and V channels a lane; D is a multiple of V: the state is read
+// and written in place, so no channel may be two wavefronts'.
 template <int E, int V>
 __global__ __launch_bounds__(256) void step_kernel(Args a, float *state, int states, const int32_t *slots, int n)
 {
@@ -801,7 +804,7 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, float *state, int sta
     const int row = unit / a.columns;
     if (row >= n)
         return;
-    const int j = min((unit % a.columns * 64 + lane) * V, a.D - V);
+    const int mine = (unit % a.columns * 64 + lane) * V, j = min(mine, a.D - V);
     const uint32_t off = (uint32_t)j * E;
     Raw<E, V> x = load<E, V>(a.x + row * a.ldx + off), r = load<E, V>(a.r + row * a.ldr + off),
               i = load<E, V>(a.i + row * a.ldi + off);
@@ -848,9 +851,11 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, float *state, int sta
         r = load<E, V>(a.r + t * a.ldr + off);
         i = load<E, V>(a.i + t * a.ldi + off);
     }
+    if (mine < a.D) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        s[(uint32_t)(j + v)] = h[v];
+        for (int v = 0; v < V; ++v)
+            s[(uint32_t)(j + v)] = h[v];
+    }
 }
 
 uint64_t size_of(int dtype) { return dtype == RECUR_DTYPE_F32 ? 4 : 2; }
@@ -1167,7 +1172,7 @@ int recur_step(const recur_config *cfg, const recur_inputs *in, const float *lam
     a.y = (uint8_t *)y;
     a.n = n;
     const bool f32 = cfg->dtype == RECUR_DTYPE_F32;
-    a.per = per_lane(a.D, n);
+    a.per = a.D % 2 ? 1 : per_lane(a.D, n);
     a.columns = (int)columns(a.D, a.per);
     const bool one = a.per == 1;
     auto k = f32 ? (one ? step_kernel<4, 1> : step_kernel<4, 2>) : (one ? step_kernel<2, 1> : step_kernel<2, 2>);

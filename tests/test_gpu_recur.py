@@ -221,6 +221,52 @@ def test_edges_of_pieces(off):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [31, 32, 33, 64, 65, 128, 129, 256, 257, 512, 513])
+def test_lengths_where_pieces_change(T, t):
+    """Sequences that cross the borders, with all that they may have; a workspace of a
+    longer call serves, and an accumulated dlam gets every channel's sum once."""
+    m = M()
+    ws = m.Workspace(m.config(90, 2000, t))
+    for off in ([0, T // 3, T // 3, T], [1, T - 1], [0, T]):
+        c = Case(T, 90, t, off, h0=True, dhT=True)
+        c.cfg.max_tokens = 2000
+        got = c.check(ws)
+        acc = m.config(90, 2000, t, accumulate=True)
+        old = torch.full((90,), 3.0, device="cuda")
+        _, _, saved = m.fwd(acc, ws, c.x, c.r, c.i, c.lam, c.offsets, c.h0, keep=True)
+        m.bwd(acc, ws, c.x, c.r, c.i, c.lam, saved, c.dy, c.offsets, c.h0, c.dhT, dlam=old)
+        assert torch.equal(old, got["dlam"] + 3.0)
+
+
+@pytest.mark.parametrize("T", [40, 200, 600])
+def test_widest(T):
+    Case(T, 16384, "bf16", [0, T // 2, T], h0=True, dhT=True).check()
+    Case(T, 16383, "f32").check()
+
+
+@pytest.mark.parametrize("T", [20, 200, 700])
+@pytest.mark.parametrize("n", [1500, 5000, 70000])
+def test_more_sequences_than_positions(n, T):
+    r = np.random.default_rng([n, T])
+    off = np.sort(r.integers(3, T - 2, n + 1))
+    Case(T, 20, "f32", off, h0=True, dhT=True).check()
+
+
+@pytest.mark.parametrize("T,lo,hi", [(60, 5, 50), (200, 33, 100), (1500, 100, 1000)])
+def test_padding_counts_for_nothing(T, lo, hi):
+    """Whatever stands in the rows in front of the first sequence and behind the last."""
+    m, D = M(), 70
+    for t in ("f32", "bf16"):
+        c = Case(T, D, t, [lo, (lo + hi) // 2, hi], h0=True, dhT=True)
+        want = c.check()
+        for v in (float("nan"), float("inf"), -float("inf")):
+            for x in (c.x, c.r, c.i, c.dy):
+                x[:lo], x[hi:] = v, v
+            got = c.run()
+            assert all(torch.equal(got[k], want[k]) for k in want), v
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("T,D,off", [(4000, 70, None), (5000, 30, [0, 4100, 5000]), (3001, 130, [0, 1, 2999, 3001])])
 def test_long(T, D, off, t):
     Case(T, D, t, off, h0=True, dhT=True).check()
@@ -403,34 +449,48 @@ def test_captured():
         torch.randn(1 << 16, device="cuda").sum().item()
 
 
+def _check_step(c, r, slots, states):
+    m, n, D = M(), c.T, c.D
+    st, hst = _dev(r.standard_normal((states, D)))
+    sd = None if slots is None else torch.from_numpy(slots.astype(np.int32)).cuda()
+    y = m.step(m.config(D, 1, c.t), c.x, c.r, c.i, c.lam, st, sd)
+    oy, ost = orc.step(c.hx, c.hr, c.hi, c.hlam, 8.0, hst, slots)
+    # the bound of a sequence: the slot's positions in order
+    a, mm, g, rho = orc.gates(c.hr, c.hi, c.hlam, 8.0)
+    re = (2 * np.abs(c.hr) + 26) * U
+    ea = U + re * np.abs(np.expm1(-8.0 * orc.softplus(c.hlam) * rho))
+    u = np.abs(mm * g * c.hx)
+    E, S = np.zeros((states, D)), np.abs(hst)
+    ey = np.zeros((n, D))
+    for k in range(n):
+        s = k if slots is None else slots[k]
+        if 0 <= s < states:
+            E[s] = a[k] * E[s] + S[s] * (ea[k] + 2 * U * a[k]) + u[k] * (re[k] + (2 * np.abs(c.hi[k]) + 14) * U)
+            S[s] = a[k] * S[s] + u[k]
+            ey[k] = E[s] + 2 * U * S[s]
+    within(st, ost, V(ost, E + 2 * U * S), "f32", "state")
+    within(y, oy, V(oy, ey), c.t, "y")
+
+
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("n,D", [(1, 768), (1, 1), (5, 65), (33, 129), (70, 768), (300, 40)])
 def test_step(n, D, t):
-    m = M()
     r = np.random.default_rng([n, D])
     c = Case(n, D, t)
     states = n + 7
     for slots in (None, r.permutation(states)[:n], r.integers(-2, states + 2, n), np.zeros(n, int), np.full(n, -1)):
-        st, hst = _dev(r.standard_normal((states, D)))
-        sd = None if slots is None else torch.from_numpy(slots.astype(np.int32)).cuda()
-        cfg = m.config(D, 1, t)
-        y = m.step(cfg, c.x, c.r, c.i, c.lam, st, sd)
-        oy, ost = orc.step(c.hx, c.hr, c.hi, c.hlam, 8.0, hst, slots)
-        # the bound of a sequence: the slot's positions in order
-        a, mm, g, rho = orc.gates(c.hr, c.hi, c.hlam, 8.0)
-        re = (2 * np.abs(c.hr) + 26) * U
-        ea = U + re * np.abs(np.expm1(-8.0 * orc.softplus(c.hlam) * rho))
-        u = np.abs(mm * g * c.hx)
-        E, S = np.zeros((states, D)), np.abs(hst)
-        ey = np.zeros((n, D))
-        for k in range(n):
-            s = k if slots is None else slots[k]
-            if 0 <= s < states:
-                E[s] = a[k] * E[s] + S[s] * (ea[k] + 2 * U * a[k]) + u[k] * (re[k] + (2 * np.abs(c.hi[k]) + 14) * U)
-                S[s] = a[k] * S[s] + u[k]
-                ey[k] = E[s] + 2 * U * S[s]
-        within(st, ost, V(ost, E + 2 * U * S), "f32", "state")
-        within(y, oy, V(oy, ey), t, "y")
+        _check_step(c, r, slots, states)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [129, 257, 258])
+def test_step_of_more_rows_than_run_at_once(D, t):
+    """Every channel's state moves on once, by whichever wavefront and whenever it runs."""
+    r = np.random.default_rng(D)
+    n = 20000
+    c = Case(n, D, t)
+    _check_step(c, r, None, n)
+    _check_step(c, r, r.permutation(n + 50)[:n], n + 50)
 
 
 def test_steps_continue_a_prompt():
