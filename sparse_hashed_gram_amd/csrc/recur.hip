@@ -780,16 +780,23 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 }
 
 // The rows of one slot: whether `row` is the first of them (it takes them all, in
-// order), and `more`: whether others follow.  The wavefront looks at 64 slots a load,
-// and waits for eight loads at once.
+// order), and `more`: whether others follow.  Eight loads of 64 slots at a time, the last
+// slot again behind the end: as many for every lane, or the rest would be loaded one by
+// one (500 rows of 2,048 channels: 8.9 us instead of 6.6; without looking 5.5).
 __device__ __forceinline__ bool first_of_slot(const int32_t *slots, int n, int row, int slot, int lane, bool &more)
 {
     bool before = false, behind = false;
-#pragma unroll 8
-    for (int k = lane; k < n; k += 64) {
-        const bool same = slots[k] == slot;
-        before = before || (same && k < row);
-        behind = behind || (same && k > row);
+    for (int at = 0; at < n; at += 512) {
+        int32_t s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[i] = slots[min(at + i * 64 + lane, n - 1)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = min(at + i * 64 + lane, n - 1);
+            before = before || (s[i] == slot && k < row);
+            behind = behind || (s[i] == slot && k > row);
+        }
     }
     more = __any(behind);
     return !__any(before);

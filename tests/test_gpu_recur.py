@@ -473,7 +473,7 @@ def _check_step(c, r, slots, states):
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
-@pytest.mark.parametrize("n,D", [(1, 768), (1, 1), (5, 65), (33, 129), (70, 768), (300, 40)])
+@pytest.mark.parametrize("n,D", [(1, 768), (1, 1), (5, 65), (33, 129), (70, 768), (300, 40), (512, 9), (1100, 66)])
 def test_step(n, D, t):
     r = np.random.default_rng([n, D])
     c = Case(n, D, t)
