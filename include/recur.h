@@ -27,8 +27,8 @@
  * Sequences: offsets (device, int32 [n + 1], ascending from >= 0 to <= T):
  * sequence k is rows offsets[k] .. offsets[k + 1] - 1; one without rows has hT =
  * h0 (or 0), dh0 = dhT (or 0).  Rows in front of the first and behind the last
- * sequence count for nothing and are left as they were in every output.  offsets NULL: n has to be 1, and the
- * sequence is all T rows.  Offsets that do not ascend give unspecified results,
+ * sequence count for nothing, whatever they hold, and are left as they were in every
+ * output.  offsets NULL: n has to be 1, and the sequence is all T rows.  Offsets that do not ascend give unspecified results,
  * but nothing outside the buffers is touched.  Nothing of one sequence reaches
  * another, NaN and infinities included; within a sequence a NaN stays.
  *

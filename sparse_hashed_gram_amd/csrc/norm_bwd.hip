@@ -1,5 +1,13 @@
 // Backward of the norms (include/norm.h), rows and, in parts, the sums over t
-// that the parameters' gradients are made of.
+// that the parameters' gradients are made of.  xh is computed again from the row (no
+// statistics are kept), so a row is read once and its gradient written once; the sums
+// over t stay in registers over all rows of a block, then go through LDS to the block's
+// part of the workspace, which one more kernel adds up in a fixed order (5 us).
+//
+// HBM bounds it at many rows: the norm of 49,152 x 768 takes 102 us of kernel (528 MB,
+// 5.2 TB/s), the join with a gate an element 161 us (830 MB, 5.1 TB/s).  4,099 x 1,001 in
+// fp32 with all gradients: 32 us (3.6 TB/s), 4 rows a block at a time and five turns of which
+// the last has three rows.
 #include <algorithm>
 
 #include "norm_dev.hpp"
@@ -71,7 +79,6 @@ template <int XE, int RE, int P, bool FULL, bool JOIN, bool EXTRA>
 struct Row {
     Piece<RE> r1[P], d1[P], r[P];
     Piece<XE> dx[P], b[P], g[P];
-
 
     __device__ __forceinline__ void load(const Args &a, int64_t row, const int (&e)[P], const int (&n)[P])
     {
@@ -285,6 +292,7 @@ template <int XE, int RE, int W, int P, bool FULL>
 int launch_as(const Args &a, bool extra, hipStream_t s)
 {
     // as many blocks as run at once: one a compute unit with the join's registers, two without
+    // (512 for the join: 36.6 us instead of 31.8 at 4,099 x 1,001)
     const int grid = (int)std::min<int64_t>((a.T + kRows<W> - 1) / kRows<W>, a.dB ? 256 : kMaxBlocks);
     auto k = a.dB ? (extra ? bwd_kernel<XE, RE, W, P, FULL, true, true> : bwd_kernel<XE, RE, W, P, FULL, true, false>)
                   : (extra ? bwd_kernel<XE, RE, W, P, FULL, false, true> : bwd_kernel<XE, RE, W, P, FULL, false, false>);

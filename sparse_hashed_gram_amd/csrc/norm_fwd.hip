@@ -1,5 +1,9 @@
 // Forward of the norms (include/norm.h): X = norm(R), and the join
-// R1 = s R + g norm(B), X = norm(R1), in one pass over the rows.
+// R1 = s R + g norm(B), X = norm(R1), in one pass over the rows: a row lives in
+// registers between its loads and its stores, the block's next rows are on their way
+// meanwhile.  HBM bounds it: the join of 49,152 x 768 with a gate an element, bf16
+// beside an fp32 stream, takes 101 us (528 MB, 5.2 TB/s; a copy reaches 5.0 to 5.2).
+// One row takes 2.1 us of kernel and 7.7 with the call.
 #include <algorithm>
 
 #include "norm_dev.hpp"
@@ -13,7 +17,6 @@ template <int XE, int RE, int P, bool FULL, bool JOIN>
 struct Row {
     Piece<RE> r[P];
     Piece<XE> b[P], g[P];
-
 
     __device__ __forceinline__ void load(const Args &a, int64_t row, const int (&e)[P], const int (&n)[P])
     {
@@ -135,6 +138,7 @@ __global__ __launch_bounds__(kThreads) void fwd_kernel(Args a)
 template <int XE, int RE, int W, int P>
 void launch(const Args &a, hipStream_t s)
 {
+    // as many blocks as run at once; rows in turns spare the rest their parameters' loads
     const unsigned grid = (unsigned)std::min<int64_t>((a.T + kRows<W> - 1) / kRows<W>, 1024);
     const bool full = a.D == 256 * W * P;
     auto k = a.R1 ? (full ? fwd_kernel<XE, RE, W, P, true, true> : fwd_kernel<XE, RE, W, P, false, true>)

@@ -1,10 +1,21 @@
 // The gated linear recurrence (include/recur.h).
 //
-// A block takes a chunk of 64 positions of 128 channels: 8 wavefronts of 8 positions,
-// a lane two channels.  A stretch of positions is h -> A h + H, so stretches join:
-// positions in registers, wavefronts through LDS, chunks through words of the
-// workspace that say by themselves when they are there (state_before).  Every input
-// is read once and every output written once.
+// A block takes a chunk of 64 positions (backward: 32) of 128 channels: 4 wavefronts of
+// 16 (8) positions, a lane two channels.  A stretch of positions is h -> A h + H, so
+// stretches join: positions in registers, wavefronts through LDS, chunks through words
+// of the workspace that say by themselves when they are there (state_before).  Every
+// input is read once and every output written once; the backward gets its states from
+// one that the forward saved every 32 positions.
+//
+// Measured (bf16, 768 channels): forward of 131,072 positions 226 us (3.6 TB/s), of
+// 49,152 92 us (3.3 TB/s); backward of 49,152 174 us (3.0 TB/s).  What bounds it is the
+// time from a chunk's stretch to the state in front of it, two trips through memory
+// that other blocks on the compute unit cover in part: without ticket and words the
+// same kernels take 67 and 127 us, their vector instructions alone 43 and 85.  Hence
+// few registers (three blocks a compute unit: 8 wavefronts of 8 positions each way, two
+// and one block, took 117 and 228 us) and little to wait for.  A grid of resident blocks
+// that load the next chunk ahead took 137 to 200 us forward: they drift apart, and one
+// that is late holds tickets that all others wait for.
 #include <algorithm>
 #include <initializer_list>
 
@@ -109,7 +120,7 @@ __device__ __forceinline__ void find_marks(const Args &a, int64_t t0, Ends mine,
     lds_barrier();
 }
 
-// The block's chunk, and its place side by side.  A block that waits for others
+// The block's chunk, and its column of channels.  A block that waits for others
 // takes its place when it begins to run, in the order in which chunks depend on
 // one another: whoever it waits for has begun before it.
 __device__ __forceinline__ void place(const Args &a, int &chunk, int &column)
@@ -177,7 +188,8 @@ struct Shared {
 // (states), so only those form a chain, and one of them hands on as soon as the one
 // before has.  A chunk takes the state in front of its group through the group's
 // earlier chunks, always in the same order: results do not depend on who came
-// first.  A wait ends: who is waited for has begun to run (place), and waits itself
+// first.  (Groups of 32 and 48: 182 and 186 us instead of 176 for the backward of
+// 49,152 positions, 28.7 and 30.4 instead of 28.4 for 4,096.)  A wait ends: who is waited for has begun to run (place), and waits itself
 // only for chunks in front of it; should one never answer, the values become NaN
 // after a bounded number of polls.
 constexpr int kPolls = 1 << 20;
@@ -362,6 +374,9 @@ __device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kFwdSteps], const
     }
 }
 
+// Rows are asked for before anything else is looked at, and stay packed until their gates
+// are computed; a_t and u_t of all positions then stay in registers until the state in
+// front is known.  One exp for each gate and one more beyond kSeries, one square root.
 template <int E, int V, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void fwd_kernel(Args a)
 {
@@ -548,7 +563,10 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const
 // Chunks from the last to the first.  The states come from the saved one, forward
 // through the chunk; with them and the gates every output is G_t times a number of
 // its position: dx c1, di c2, dr cr, and rho dz (of dlam) cl.  G in turn runs
-// backwards, what a position hands on being a_t G_t.
+// backwards, what a position hands on being a_t G_t.  Those four numbers are all that
+// the registers keep over the wait (168 of them with bf16).  One channel a lane and 16
+// positions instead: 358 us of 49,152 x 768 instead of 176 (spills, and half the bytes a
+// load).
 template <int E, int V, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void bwd_kernel(Args a)
 {
@@ -879,7 +897,9 @@ int check_config(const recur_config *c)
 
 int64_t saved_rows(int64_t T) { return (T + RECUR_CHUNK - 1) / RECUR_CHUNK; }
 // Wavefronts of a block: the usual ones, or many where a call that they have not room
-// for is then one chunk, with no words to clear and nobody to wait for.
+// for is then one chunk, with no words to clear and nobody to wait for (calls back to
+// back, 768 channels: forward of 100 positions 11.6 us instead of 14.6, of 250 11.5 instead
+// of 14.3, forward and backward of 100 26.4 instead of 35.1).
 int waves(int pass, int64_t T)
 {
     const int steps = pass == RECUR_PASS_FWD ? kFwdSteps : kBwdSteps;
@@ -890,14 +910,15 @@ int64_t chunks(int pass, int64_t T) { return (T + chunk_of(pass, T) - 1) / chunk
 uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // Channels of a lane: two, but one up to 64 channels, where half the wavefront would
-// have none, and for few rows of chunks (or a step's rows).
+// have none, and for few blocks (or a step's rows), which then are twice as many
+// (backward of 200 x 768 in chunks, 42 blocks: 8.6 us instead of 11.3; of 2,048 x 768, 384
+// blocks: 20.4 instead of 18.3; forward of it, 192 blocks: 12.6 instead of 11.4).
 constexpr int64_t kFewBlocks = 64;
 int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <= kFewBlocks ? 1 : 2; }
 int64_t columns(int D, int per) { return (D + 64 * per - 1) / (64 * per); }
 
 // Workspace: the ticket, the words of n chunks and their groups, the backward's
-// parts of dlam.
-// Words of a row of chunks: enough for one or two channels a lane.
+// parts of dlam.  Words of a row of chunks: enough for one or two channels a lane.
 uint64_t row_words(int D) { return (uint64_t)columns(D, 2) * 128; }
 uint64_t words_of(int D, int64_t n) { return (uint64_t)(n + n / kGroup + 1) * row_words(D); }
 uint64_t ws_need(const recur_config *c, int pass)
@@ -994,7 +1015,7 @@ void place_words(Args &a, int pass, void *ws)
 {
     uint8_t *p = (uint8_t *)ws;
     const int64_t n = chunks(pass, a.T);
-    a.per = n <= 1 ? 1 : per_lane(a.D, n);   // 1,024 threads have 128 registers
+    a.per = n <= 1 ? 1 : per_lane(a.D, n);   // one chunk may have 1,024 threads: 128 registers
     a.columns = (int)columns(a.D, a.per);
     a.chunks = (int)n;
     a.alone = n <= 1;

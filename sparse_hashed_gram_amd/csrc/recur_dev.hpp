@@ -10,7 +10,8 @@
 
 namespace recur {
 
-// A block takes a chunk of WAVES * STEPS positions, STEPS to a wavefront.
+// A block takes a chunk of WAVES * STEPS positions, STEPS to a wavefront (13 to 20 in the
+// forward: the same times).
 constexpr int kWaves = 4, kFwdSteps = 16, kBwdSteps = 8;
 constexpr int kManyWaves = 16;   // where that makes one chunk of the whole call
 static_assert(kWaves * kBwdSteps == RECUR_CHUNK, "a saved state in front of every backward chunk");
@@ -98,7 +99,7 @@ __device__ __forceinline__ float alone(float a, float b)
 
 // The value is computed where this stands.  Otherwise the compiler moves a product
 // down to the branch that uses it, and its factors stay in registers until then (256
-// registers and spills instead of 155 to 169 in the backward).
+// registers and spills instead of 168 in the backward).
 __device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
 
 // a = 1 + e and m = sqrt(1 - a^2) = sqrt(-e (2 + e)) with e = exp(z) - 1, so that
