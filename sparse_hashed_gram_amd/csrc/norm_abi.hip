@@ -371,8 +371,8 @@ int norm_join_fwd(const norm_config *cfg, const void *R, const void *B, const no
     a.X = out(X);
     a.post = post;
     a.pre = pre;
-    a.p.post_w = in(p->post_w);
-    a.p.post_b = in(p->post_b);
+    a.p.post_w = post ? in(p->post_w) : nullptr;
+    a.p.post_b = post ? in(p->post_b) : nullptr;
     a.p.gate = cfg->gate == NORM_BY_NONE || token ? nullptr : in(p->gate);
     a.p.scale = cfg->scale == NORM_BY_NONE ? nullptr : in(p->scale);
     a.p.w = pre ? in(p->w) : nullptr;

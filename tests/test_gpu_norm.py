@@ -247,6 +247,20 @@ def test_many_rows(T):
         _check_join(Case(T, 1100, "rms", ("bf16", "f32"), "token", "none", bias=False))
 
 
+def test_parameters_of_norms_that_the_config_has_not():
+    """The C ABI takes no notice of them."""
+    import ctypes
+    c = Case(9, 500, "rms", ("bf16", "f32"), "vector", "none", pre=False, post=False)
+    n, cfg = N(), c.cfg()
+    want = n.join_fwd(cfg, c.dev["R"], c.dev["B"], **c.params())[0]
+    nan = torch.full((500,), float("nan"), device="cuda")
+    got = torch.empty_like(want)
+    p = n.NormParams(nan.data_ptr(), nan.data_ptr(), c.dev["gate"].data_ptr(), None, nan.data_ptr(), nan.data_ptr())
+    assert n.lib().norm_join_fwd(ctypes.byref(cfg), c.dev["R"].data_ptr(), c.dev["B"].data_ptr(), ctypes.byref(p), 9,
+                                 got.data_ptr(), None, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(got, want)
+
+
 def test_without_the_stream_gradient():
     c = Case(11, 768, "rms", ("bf16", "f32"), gate="token", bias=False)
     n, z = N(), torch.zeros(11, 768, device="cuda")
