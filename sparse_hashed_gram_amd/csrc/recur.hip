@@ -120,20 +120,22 @@ __device__ __forceinline__ void find_marks(const Args &a, int64_t t0, Ends mine,
     lds_barrier();
 }
 
-// The block's chunk, and its column of channels.  A block that waits for others
-// takes its place when it begins to run, in the order in which chunks depend on
-// one another: whoever it waits for has begun before it.
+// The block's chunk, and its column of channels.  A block that waits for others takes
+// its chunk when it begins to run, in the order in which a column's chunks depend on one
+// another: whoever it waits for has begun before it.  A ticket a column, each in a line of
+// its own: one address gives out a number every 18 ns, which with one ticket for all was
+// what bounded the kernels.
 __device__ __forceinline__ void place(const Args &a, int &chunk, int &column)
 {
     __shared__ uint32_t ticket;
     chunk = 0;
     column = blockIdx.x;
     if (!a.alone) {
+        column = blockIdx.x % (uint32_t)a.columns;
         if (threadIdx.x == 0)
-            ticket = atomicAdd(a.ticket, 1u);
+            ticket = atomicAdd(a.tickets + column * kTicketWords, 1u);
         __syncthreads();
-        chunk = (int)(ticket / (uint32_t)a.columns);
-        column = (int)(ticket % (uint32_t)a.columns);
+        chunk = (int)ticket;
     }
 }
 
@@ -318,8 +320,8 @@ __global__ __launch_bounds__(256) void clear_kernel(Args a, const float *in, flo
         ulonglong2 *sums = reinterpret_cast<ulonglong2 *>(a.sums);   // sums, then states: a multiple of 64 words
         for (int64_t k = first; k < a.words / 2; k += step)
             sums[k] = make_ulonglong2(kNone, kNone);
-        if (first == 0)
-            *a.ticket = 0;
+        for (int64_t k = first; k < a.columns; k += step)
+            a.tickets[k * kTicketWords] = 0;
     }
     if (out) {
         for (int64_t s = blockIdx.x; s < a.n; s += gridDim.x) {
@@ -917,14 +919,16 @@ constexpr int64_t kFewBlocks = 64;
 int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <= kFewBlocks ? 1 : 2; }
 int64_t columns(int D, int per) { return (D + 64 * per - 1) / (64 * per); }
 
-// Workspace: the ticket, the words of n chunks and their groups, the backward's
+// Workspace: the tickets, the words of n chunks and their groups, the backward's
 // parts of dlam.  Words of a row of chunks: enough for one or two channels a lane.
 uint64_t row_words(int D) { return (uint64_t)columns(D, 2) * 128; }
 uint64_t words_of(int D, int64_t n) { return (uint64_t)(n + n / kGroup + 1) * row_words(D); }
+// One or two channels a lane: no more columns than 64 channels each make.
+uint64_t ticket_bytes(int D) { return align_up((uint64_t)columns(D, 1) * kTicketWords * 4); }
 uint64_t ws_need(const recur_config *c, int pass)
 {
     const int64_t n = chunks(pass, c->max_tokens);
-    return kAlign + align_up(words_of(c->dim, n) * 8) + (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
+    return ticket_bytes(c->dim) + align_up(words_of(c->dim, n) * 8) + (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
 }
 
 struct Buf {
@@ -1020,10 +1024,11 @@ void place_words(Args &a, int pass, void *ws)
     a.chunks = (int)n;
     a.alone = n <= 1;
     a.words = (int64_t)words_of(a.D, n);
-    a.ticket = (uint32_t *)p;
-    a.sums = (uint64_t *)(p + kAlign);
+    a.tickets = (uint32_t *)p;
+    p += ticket_bytes(a.D);
+    a.sums = (uint64_t *)p;
     a.states = a.sums + n * (int64_t)row_words(a.D);
-    a.part = (float *)(p + kAlign + align_up((uint64_t)a.words * 8));
+    a.part = (float *)(p + align_up((uint64_t)a.words * 8));
 }
 
 // What has to be done before the chunks; states without rows: out = in.

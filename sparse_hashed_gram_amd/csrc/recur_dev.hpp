@@ -15,6 +15,7 @@ namespace recur {
 constexpr int kWaves = 4, kFwdSteps = 16, kBwdSteps = 8;
 constexpr int kManyWaves = 16;   // where that makes one chunk of the whole call
 static_assert(kWaves * kBwdSteps == RECUR_CHUNK, "a saved state in front of every backward chunk");
+constexpr int kTicketWords = 64;   // from one column's ticket to the next
 constexpr int kGroup = 16;   // chunks between two states that are passed on
 
 struct Args {
@@ -31,7 +32,7 @@ struct Args {
     bool alone;              // one chunk: nobody waits
     float c;
     // workspace
-    uint32_t *ticket;
+    uint32_t *tickets;  // [columns], kTicketWords apart
     uint64_t *sums;     // [chunks][columns][V][64]: a chunk's (A, H)
     uint64_t *states;   // [chunks / kGroup + 1][columns][V][64]: the state in front of a group
     int64_t words;      // of both
