@@ -64,7 +64,7 @@ extern "C" {
                             without offsets), a distance between rows under D or
                             over 2^31 - 1, a workspace too small, or 2^23 and
                             more blocks: pieces of 32 (forward: 64) positions by
-                            128 (D up to 64: 64) channels                      */
+                            128 (D up to 64, backward of fp32: 64) channels    */
 #define RECUR_EARG -5    /* an output that overlaps an operand or another output,
                             or an unknown pass                                 */
 #define RECUR_EHIP -6    /* the HIP runtime reported an error                  */

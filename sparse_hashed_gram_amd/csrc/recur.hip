@@ -570,7 +570,7 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const
 // positions instead: 358 us of 49,152 x 768 instead of 176 (spills, and half the bytes a
 // load).
 template <int E, int V, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void bwd_kernel(Args a)
+__global__ __launch_bounds__(WAVES * 64, WAVES == kWaves ? 3 : 2) void bwd_kernel(Args a)
 {
     constexpr int STEPS = kBwdSteps, N = WAVES * STEPS;
     __shared__ Shared<V, WAVES, STEPS> sh;
@@ -912,11 +912,20 @@ int64_t chunks(int pass, int64_t T) { return (T + chunk_of(pass, T) - 1) / chunk
 uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
 // Channels of a lane: two, but one up to 64 channels, where half the wavefront would
-// have none, and for few blocks (or a step's rows), which then are twice as many
-// (backward of 200 x 768 in chunks, 42 blocks: 8.6 us instead of 11.3; of 2,048 x 768, 384
-// blocks: 20.4 instead of 18.3; forward of it, 192 blocks: 12.6 instead of 11.4).
-constexpr int64_t kFewBlocks = 64;
+// have none, and for as few blocks (or rows of a step) that twice as many still run at once
+// (backward of 2,048 x 768 bf16, 384 blocks: 13.8 us instead of 16.0; of 3,000, 564: 20.2
+// instead of 19.8; forward of 4,096, 384: 12.8 instead of 15.1; of 6,000, 564: 19.6 instead
+// of 18.7; backward of 49,152: 196 instead of 171).
+constexpr int64_t kFewBlocks = 400;
 int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <= kFewBlocks ? 1 : 2; }
+// Of a pass: one too where the call is one chunk, whose 1,024 threads have 128 registers,
+// and in the backward of fp32, where two take 190, two blocks a compute unit instead of
+// four (4,096 x 768: 25.3 us instead of 29.0, 16,384: 84.9 instead of 88.7, 49,152: 252
+// instead of 254; the forward's 168 leave it three, and of 49,152 it takes 133 instead of 139).
+int per_lane(const recur_config *c, int pass, int64_t n)
+{
+    return n <= 1 || (pass == RECUR_PASS_BWD && c->dtype == RECUR_DTYPE_F32) ? 1 : per_lane(c->dim, n);
+}
 int64_t columns(int D, int per) { return (D + 64 * per - 1) / (64 * per); }
 
 // Workspace: the tickets, the words of n chunks and their groups, the backward's
@@ -992,7 +1001,7 @@ int check_call(const recur_config *cfg, int pass, const void *ws, uint64_t ws_by
         return RECUR_EALIGN;
     if (T < 0 || T > cfg->max_tokens || n < 0 || n > (int64_t(1) << 24) || (!offsets && n != 1) ||
         bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi) || ws_bytes < ws_need(cfg, pass) ||
-        chunks(pass, T) * columns(cfg->dim, 2) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
+        chunks(pass, T) * columns(cfg->dim, per_lane(cfg, pass, chunks(pass, T))) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
         return RECUR_ESIZE;
     return RECUR_OK;
 }
@@ -1015,11 +1024,11 @@ Args base(const recur_config *c, const recur_inputs *in, const float *lam, int64
     return a;
 }
 
-void place_words(Args &a, int pass, void *ws)
+void place_words(const recur_config *c, Args &a, int pass, void *ws)
 {
     uint8_t *p = (uint8_t *)ws;
     const int64_t n = chunks(pass, a.T);
-    a.per = n <= 1 ? 1 : per_lane(a.D, n);   // one chunk may have 1,024 threads: 128 registers
+    a.per = per_lane(c, pass, n);
     a.columns = (int)columns(a.D, a.per);
     a.chunks = (int)n;
     a.alone = n <= 1;
@@ -1115,7 +1124,7 @@ int recur_fwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
     a.y = (uint8_t *)y;
     a.hT = hT;
     a.saved = saved;
-    place_words(a, RECUR_PASS_FWD, ws);
+    place_words(cfg, a, RECUR_PASS_FWD, ws);
     hipStream_t s = (hipStream_t)stream;
     clear(a, h0, hT, s);
     if (T) {
@@ -1168,14 +1177,14 @@ int recur_bwd(const recur_config *cfg, void *ws, uint64_t ws_bytes, const recur_
         a.T = T = 0;
     if (T == 0 && a.accum && !dh0)
         return RECUR_OK;
-    place_words(a, RECUR_PASS_BWD, ws);
+    place_words(cfg, a, RECUR_PASS_BWD, ws);
     hipStream_t s = (hipStream_t)stream;
     clear(a, dhT, dh0, s);
     if (T) {
         const bool f32 = cfg->dtype == RECUR_DTYPE_F32, one = a.per == 1;
         const int w = waves(RECUR_PASS_BWD, T);
         auto k = w == kManyWaves ? (f32 ? bwd_kernel<4, 1, kManyWaves> : bwd_kernel<2, 1, kManyWaves>)
-                 : f32           ? (one ? bwd_kernel<4, 1, kWaves> : bwd_kernel<4, 2, kWaves>)
+                 : f32           ? bwd_kernel<4, 1, kWaves>
                                  : (one ? bwd_kernel<2, 1, kWaves> : bwd_kernel<2, 2, kWaves>);
         k<<<(unsigned)(chunks(RECUR_PASS_BWD, T) * a.columns), w * 64, 0, s>>>(a);
     }
