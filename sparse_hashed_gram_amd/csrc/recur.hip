@@ -7,10 +7,10 @@
 // input is read once and every output written once; the backward gets its states from
 // one that the forward saved every 32 positions.
 //
-// Measured (bf16, 768 channels): forward of 131,072 positions 226 us (3.6 TB/s), of
-// 49,152 92 us (3.3 TB/s); backward of 49,152 174 us (3.0 TB/s).  What bounds it is the
+// Measured (bf16, 768 channels): forward of 131,072 positions 225 us (3.6 TB/s), of
+// 49,152 87 us (3.5 TB/s); backward of 49,152 171 us (3.1 TB/s).  What bounds it is the
 // time from a chunk's stretch to the state in front of it, two trips through memory
-// that other blocks on the compute unit cover in part: without ticket and words the
+// that other blocks on the compute unit cover in part: without tickets and words the
 // same kernels take 67 and 127 us, their vector instructions alone 43 and 85.  Hence
 // few registers (three blocks a compute unit: 8 wavefronts of 8 positions each way, two
 // and one block, took 117 and 228 us) and little to wait for.  A grid of resident blocks
@@ -123,8 +123,9 @@ __device__ __forceinline__ void find_marks(const Args &a, int64_t t0, Ends mine,
 // The block's chunk, and its column of channels.  A block that waits for others takes
 // its chunk when it begins to run, in the order in which a column's chunks depend on one
 // another: whoever it waits for has begun before it.  A ticket a column, each in a line of
-// its own: one address gives out a number every 18 ns, which with one ticket for all was
-// what bounded the kernels.
+// its own: one address gives out a number every 18 ns, which with one ticket for all
+// bounded the kernels (backward of 4,096 x 768 28.1 us instead of 21.2, forward of 16,384
+// 42.9 instead of 34.4).
 __device__ __forceinline__ void place(const Args &a, int &chunk, int &column)
 {
     __shared__ uint32_t ticket;
@@ -190,8 +191,8 @@ struct Shared {
 // (states), so only those form a chain, and one of them hands on as soon as the one
 // before has.  A chunk takes the state in front of its group through the group's
 // earlier chunks, always in the same order: results do not depend on who came
-// first.  (Groups of 32 and 48: 182 and 186 us instead of 176 for the backward of
-// 49,152 positions, 28.7 and 30.4 instead of 28.4 for 4,096.)  A wait ends: who is waited for has begun to run (place), and waits itself
+// first.  (Groups of 32 and 64: 175 and 210 us instead of 171 for the backward of
+// 49,152 positions, 21.9 and 28.0 instead of 21.3 for 4,096.)  A wait ends: who is waited for has begun to run (place), and waits itself
 // only for chunks in front of it; should one never answer, the values become NaN
 // after a bounded number of polls.
 constexpr int kPolls = 1 << 20;
