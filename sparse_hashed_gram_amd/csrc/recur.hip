@@ -192,9 +192,9 @@ struct Shared {
 // before has.  A chunk takes the state in front of its group through the group's
 // earlier chunks, always in the same order: results do not depend on who came
 // first.  (Groups of 32 and 64: 175 and 210 us instead of 171 for the backward of
-// 49,152 positions, 21.9 and 28.0 instead of 21.3 for 4,096.)  A wait ends: who is waited for has begun to run (place), and waits itself
-// only for chunks in front of it; should one never answer, the values become NaN
-// after a bounded number of polls.
+// 49,152 positions, 21.9 and 28.0 instead of 21.3 for 4,096.)  A wait ends: who is
+// waited for has begun to run (place), and waits itself only for chunks in front of it;
+// should one never answer, the values become NaN after a bounded number of polls.
 constexpr int kPolls = 1 << 20;
 
 __device__ __forceinline__ uint64_t wait_for(const uint64_t *p, uint64_t w)
@@ -938,7 +938,8 @@ uint64_t ticket_bytes(int D) { return align_up((uint64_t)columns(D, 1) * kTicket
 uint64_t ws_need(const recur_config *c, int pass)
 {
     const int64_t n = chunks(pass, c->max_tokens);
-    return ticket_bytes(c->dim) + align_up(words_of(c->dim, n) * 8) + (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
+    return ticket_bytes(c->dim) + align_up(words_of(c->dim, n) * 8) +
+           (pass == RECUR_PASS_BWD ? align_up((uint64_t)n * c->dim * 4) : 0);
 }
 
 struct Buf {
@@ -1001,10 +1002,10 @@ int check_call(const recur_config *cfg, int pass, const void *ws, uint64_t ws_by
     if ((uintptr_t)ws % kAlign || (uintptr_t)offsets % 4)
         return RECUR_EALIGN;
     if (T < 0 || T > cfg->max_tokens || n < 0 || n > (int64_t(1) << 24) || (!offsets && n != 1) ||
-        bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi) || ws_bytes < ws_need(cfg, pass) ||
-        chunks(pass, T) * columns(cfg->dim, per_lane(cfg, pass, chunks(pass, T))) >= (int64_t(1) << 23))   // a launch counts its threads in 32 bits
+        bad_ld(cfg, in->ldx) || bad_ld(cfg, in->ldr) || bad_ld(cfg, in->ldi) || ws_bytes < ws_need(cfg, pass))
         return RECUR_ESIZE;
-    return RECUR_OK;
+    const int64_t count = chunks(pass, T);   // a launch counts its threads in 32 bits
+    return count * columns(cfg->dim, per_lane(cfg, pass, count)) < (int64_t(1) << 23) ? RECUR_OK : RECUR_ESIZE;
 }
 
 Args base(const recur_config *c, const recur_inputs *in, const float *lam, int64_t T)

@@ -133,6 +133,12 @@ def test_too_many_pieces(M):
     g = M.RecurGrads(1 << 55, 1 << 56, 1 << 57, 16384, 16384, 16384)
     assert M.lib().recur_bwd(c, 1 << 53, n, i, A[0], None, 1, None, 1 << 58, 1 << 54, None, 1 << 24, g, A[1], None,
                              None) == -4
+    # the backward of fp32 takes half the channels to a block: too many where the forward's are not
+    f = M.config(1024, 1 << 24, "f32")
+    n, g = M.workspace_bytes(f), M.RecurGrads(1 << 55, 1 << 56, 1 << 57, 1024, 1024, 1024)
+    i = M.RecurInputs(1 << 50, 1 << 51, 1 << 52, 1024, 1024, 1024)
+    assert M.lib().recur_bwd(f, 1 << 53, n, i, A[0], None, 1, None, 1 << 58, 1 << 54, None, 1 << 24, g, A[1], None,
+                             None) == -4
 
 
 def test_step_refusals(M):
