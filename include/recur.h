@@ -33,8 +33,9 @@
  * another, NaN and infinities included; within a sequence a NaN stays.
  *
  * Precision: fp32 inside, states and sums over t too; a and 1 - a^2 keep their
- * relative precision where a is near 1; y, dx, dr and di are rounded once (bf16:
- * nearest, ties to even).  The backward computes the gates and states again.
+ * relative precision for fast decays and for slow ones (an a or a gate below 2^-126
+ * counts as 0); y, dx, dr and di are rounded once (bf16: nearest, ties to even).
+ * The backward computes the gates and states again.
  *
  * Conventions: device pointers unless marked "host"; the caller owns every
  * buffer; calls only enqueue on `stream` (a hipStream_t, NULL = the null

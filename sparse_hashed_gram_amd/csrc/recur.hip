@@ -354,22 +354,34 @@ __device__ __forceinline__ void load_rows(const uint8_t *p, int64_t ld, int64_t 
     }
 }
 
-template <int E, int V, bool ALL>
+// all: every z of the wavefront is above kSeries.  A branch a position on it, not one
+// around them all: with two copies of the loop behind one branch the results cannot take
+// the packed rows' registers (172 instead of 137 with fp32, 136 us instead of 128 for
+// 49,152 x 768; bf16 with a channel of fast decay 94 instead of 90).
+template <int E, int V>
 __device__ __forceinline__ void fwd_gates(const Raw<E, V> (&x)[kFwdSteps], const Raw<E, V> (&r)[kFwdSteps],
-                                          const Raw<E, V> (&i)[kFwdSteps], const float (&rate)[V], float (&av)[kFwdSteps][V],
-                                          float (&u)[kFwdSteps][V])
+                                          const Raw<E, V> (&i)[kFwdSteps], const float (&rate)[V], bool all,
+                                          float (&av)[kFwdSteps][V], float (&u)[kFwdSteps][V])
 {
 #pragma unroll
     for (int k = 0; k < kFwdSteps; ++k) {
-        float xf[V], rf[V], gf[V];
+        float xf[V], rf[V], gf[V], z[V], e[V];
         unpack<E, V>(x[k], xf);
         unpack<E, V>(r[k], rf);
         unpack<E, V>(i[k], gf);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float m;
-            decays<ALL>(rate[v] * sigmoid(rf[v]), av[k][v], m);
-            u[k][v] = m * sigmoid(gf[v]) * xf[v];
+            z[v] = rate[v] * sigmoid(rf[v]);
+            decay_near(z[v], av[k][v], e[v]);
+        }
+        if (!all) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                decay_any(z[v], av[k][v], e[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            u[k][v] = rest_of(e[v]) * sigmoid(gf[v]) * xf[v];
             here(av[k][v]);
             here(u[k][v]);
         }
@@ -416,10 +428,7 @@ __global__ __launch_bounds__(WAVES * 64, E == 2 && WAVES == kWaves ? 3 : 2) void
 #pragma unroll
     for (int v = 0; v < V; ++v)
         all = all && rate[v] > kSeries;
-    if (__all(all))
-        fwd_gates<E, V, true>(x, r, i, rate, av, u);
-    else
-        fwd_gates<E, V, false>(x, r, i, rate, av, u);
+    fwd_gates<E, V>(x, r, i, rate, __all(all), av, u);
     Span1 own[V];
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -922,7 +931,7 @@ int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <
 // Of a pass: one too where the call is one chunk, whose 1,024 threads have 128 registers,
 // and in the backward of fp32, where two take 190, two blocks a compute unit instead of
 // four (4,096 x 768: 25.3 us instead of 29.0, 16,384: 84.9 instead of 88.7, 49,152: 252
-// instead of 254; the forward's 168 leave it three, and of 49,152 it takes 133 instead of 139).
+// instead of 254; the forward's 137 leave it three, and of 49,152 it takes 128 instead of 139).
 int per_lane(const recur_config *c, int pass, int64_t n)
 {
     return n <= 1 || (pass == RECUR_PASS_BWD && c->dtype == RECUR_DTYPE_F32) ? 1 : per_lane(c->dim, n);

@@ -55,23 +55,17 @@ __device__ __forceinline__ void sigmoid(float v, float &s, float &rest)
     rest = v >= 0.0f ? p : q;
 }
 
-// exp(z) - 1 for z <= 0: the series to z^7 above kSeries (what it leaves out is
-// below 2^-25 of the value), else through exp, which is below 0.71 there.  ALL: z
-// is known to be above kSeries, which saves a quarter of the gates' instructions.
+// exp(z) - 1 for z <= 0 near 0: the series to z^7, which above kSeries leaves out less
+// than 2^-25 of the value.
 constexpr float kSeries = -0.35f;
-template <bool ALL>
-__device__ __forceinline__ float expm1_neg(float z)
+__device__ __forceinline__ float expm1_near(float z)
 {
     float p = __builtin_fmaf(z, 1.0f / 5040, 1.0f / 720);
     p = __builtin_fmaf(z, p, 1.0f / 120);
     p = __builtin_fmaf(z, p, 1.0f / 24);
     p = __builtin_fmaf(z, p, 1.0f / 6);
     p = __builtin_fmaf(z, p, 0.5f);
-    p = __builtin_fmaf(z * z, p, z);
-    if constexpr (ALL)
-        return p;
-    else
-        return z > kSeries ? p : __builtin_amdgcn_exp2f(z * kLog2e) - 1.0f;
+    return __builtin_fmaf(z * z, p, z);
 }
 
 // -c sp(lam), sp(lam) = max(lam, 0) + log(1 + w) with w = exp(-|lam|), and log(1 + w)
@@ -103,14 +97,34 @@ __device__ __forceinline__ float alone(float a, float b)
 // registers and spills instead of 168 in the backward).
 __device__ __forceinline__ void here(float &v) { asm volatile("" : "+v"(v)); }
 
-// a = 1 + e and m = sqrt(1 - a^2) = sqrt(-e (2 + e)) with e = exp(z) - 1, so that
-// both keep their relative precision where a is near 1.
+// a = exp(z), e = a - 1 and m = sqrt(1 - a^2) = sqrt(-e (2 + e)).  Near 1 the series gives
+// e, and a = 1 + e; from kSeries on exp gives a, which is below 0.71 there, and e = a - 1:
+// each of them keeps its relative precision, however fast or slow the decay.  (1 + e on
+// both sides would leave a an absolute error of 2^-24, and make it 0 from z = -17.5 on.)
+__device__ __forceinline__ void decay_near(float z, float &a, float &e)
+{
+    e = expm1_near(z);
+    a = 1.0f + e;
+}
+// The same of any z <= 0, after decay_near.
+__device__ __forceinline__ void decay_any(float z, float &a, float &e)
+{
+    const float x = __builtin_amdgcn_exp2f(z * kLog2e);
+    const bool near = z > kSeries;
+    a = near ? a : x;
+    e = near ? e : x - 1.0f;
+}
+__device__ __forceinline__ float rest_of(float e) { return __builtin_amdgcn_sqrtf(-e * (2.0f + e)); }
+
+// ALL: z is known to be above kSeries, which saves a quarter of the gates' instructions.
 template <bool ALL>
 __device__ __forceinline__ void decays(float z, float &a, float &m)
 {
-    const float e = expm1_neg<ALL>(z);
-    a = 1.0f + e;
-    m = __builtin_amdgcn_sqrtf(-e * (2.0f + e));
+    float e;
+    decay_near(z, a, e);
+    if constexpr (!ALL)
+        decay_any(z, a, e);
+    m = rest_of(e);
 }
 
 // V channels side by side as floats.  Rows start at any element: the access
