@@ -559,8 +559,9 @@ __device__ __forceinline__ void bwd_gates(const Raw<E, V> (&x)[kBwdSteps], const
             c2[k][v] = c1[k][v] * xf[v] * g_rest;
             cl[k][v] = rho;
             cr[k][v] = z * rho_rest;
-            // where m is 0, z is too, and with it what this is multiplied by
-            c3[k][v] = g * xf[v] * (av[k][v] * av[k][v] * __builtin_amdgcn_rcpf(fmaxf(m, 1e-18f)));
+            // 0 where m is (z is too): a large number instead would make an infinity of a large x
+            const float over = m > 0.0f ? __builtin_amdgcn_rcpf(m) : 0.0f;
+            c3[k][v] = g * xf[v] * (av[k][v] * av[k][v] * over);
             here(av[k][v]);
             here(c1[k][v]);
             here(c2[k][v]);
