@@ -30,7 +30,8 @@
  * Precision: fp32 inside, the rows' sums and the sums over t too; each result is
  * rounded once (bf16: nearest, ties to even).  X is the norm of R1 as it is
  * before it is rounded to r_dtype; the backward takes R1 as it was stored.  A row
- * whose squares pass fp32's range is normalised all the same.  A NaN or an
+ * whose squares pass fp32's range is normalised all the same, with LAYER to 0 where
+ * all its values are one.  A NaN or an
  * infinity makes its own row NaN (and the parameters' gradients), no other.
  *
  * Conventions: device pointers unless marked "host"; the caller owns every

@@ -183,13 +183,15 @@ struct RowSum {
 // Turns v into xh in place; returns the factor rho that a gradient in front of
 // the norm has.  The mean first, then the squares of what is left: no
 // difference of large sums.  A row whose squares pass fp32's range (values over
-// about 2^63) is scaled by 2^-80 before, and its eps no longer counts.  n[p]:
-// elements of the row that piece p has, at most 4.
+// about 2^63) is scaled by 2^-80 before, and its eps no longer counts, unless all its
+// values are the same and there is a mean to take away.  n[p]: elements of the row that
+// piece p has, at most 4.
 template <int W, int P, bool FULL>
 __device__ __forceinline__ float normalise(float (&v)[P][4], const int (&n)[P], int layer, float inv_d, float eps,
                                            RowSum<W> &sum)
 {
     float q = 0.0f, m = 0.0f, unit = 1.0f;
+    const float given = eps;
     auto squares = [&] {
         q = 0.0f;
 #pragma unroll
@@ -227,11 +229,27 @@ __device__ __forceinline__ float normalise(float (&v)[P][4], const int (&n)[P], 
             eps = 0.0f;
             scale(unit);
         }
+        if (layer) {   // from the first element on: a row of one value is exactly 0
+            float x = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v[0][0])));
+            if constexpr (W > 1)
+                x = sum((int)threadIdx.x == sum.row * W * 64 ? x : 0.0f);
+            if (!(q < limit)) {
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[p][k] = FULL || k < n[p] ? v[p][k] - x : 0.0f;
+            }
+        }
         squares();
         total();
         const float2 s = sum(q, m);
         q = s.x;
         m = s.y;
+        if (layer && q == 0.0f) {   // then nothing but eps counts
+            eps = given;
+            unit = 1.0f;
+        }
     }
     if (layer) {
         m *= inv_d;
