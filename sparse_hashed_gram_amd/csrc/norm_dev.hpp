@@ -244,7 +244,7 @@ __device__ __forceinline__ float normalise(float (&v)[P][4], const int (&n)[P], 
         squares();
         total();
         const float2 s = sum(q, m);
-        q = s.x;
+        q = s.x < INFINITY ? s.x : NAN;   // of an infinity: rho 0 would make its row zeros
         m = s.y;
         if (layer && q == 0.0f) {   // then nothing but eps counts
             eps = given;

@@ -1,5 +1,5 @@
 """Norms of rows that leave fp32's range of squares: rows of one huge value, whose
-deviations from their mean are 0."""
+deviations from their mean are 0, and rows with an infinity."""
 import numpy as np
 import pytest
 import torch
@@ -78,3 +78,51 @@ def test_constant_rows_of_a_block(D):
     assert torch.equal(a[0], z[0]) and torch.equal(a[1], z[1])
     g, h = (n.join_bwd(cfg, ws, None, v, a[0], dX, R, **p) for v in (B, zero))
     assert all(torch.equal(g[k], h[k]) for k in h)
+
+
+@pytest.mark.parametrize("D", [5, 64, 768, 1000, 1500, 4096])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_not_finite_rows(kind, D):
+    """A NaN or an infinity in a row makes its norm NaN, all of it, and the row's gradient;
+    no other row."""
+    n = N()
+    T = 9
+    cfg = n.config(D, kind)
+    ws = n.Workspace(cfg)
+    R, dX = _rows(T, D, torch.float32), _rows(T, D, torch.bfloat16, 1)
+    w, b = 1 + 0.1 * _rows(1, D, torch.float32, 3)[0], _rows(1, D, torch.float32, 4)[0]
+    X0, g0 = n.fwd(cfg, R, w, b), n.bwd(cfg, ws, R, dX, w, b)
+    keep = torch.arange(T, device="cuda") != 4
+    for where in (0, D // 2, D - 1, slice(None)):
+        for v in (float("inf"), -float("inf"), float("nan")):
+            S = R.clone()
+            S[4, where] = v
+            X, g = n.fwd(cfg, S, w, b), n.bwd(cfg, ws, S, dX, w, b)
+            assert torch.equal(X[keep], X0[keep]) and torch.equal(g["dR"][keep], g0["dR"][keep])
+            assert torch.isnan(X[4]).all() and torch.isnan(g["dR"][4]).all() and torch.isnan(g["dw"]).all()
+            assert torch.equal(g["db"], g0["db"])
+    S = R.clone()
+    S[4, 0], S[4, 1:] = float("inf"), 2.0 ** 100
+    assert torch.isnan(n.fwd(cfg, S, w, b)[4]).all()
+
+
+@pytest.mark.parametrize("D", [64, 1000])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_not_finite_rows_of_a_block(kind, D):
+    n = N()
+    T = 9
+    cfg = n.config(D, kind, gate="token")
+    ws = n.Workspace(cfg)
+    R, B, dX, G = (_rows(T, D, t, k) for k, t in enumerate((torch.float32, *3 * (torch.bfloat16,))))
+    clean = n.join_fwd(cfg, R, B, gate=G)
+    keep = torch.arange(T, device="cuda") != 2
+    for v in (float("inf"), -float("inf"), float("nan")):
+        S = B.clone()
+        S[2, D // 3] = v
+        R1, X = n.join_fwd(cfg, R, S, gate=G)
+        assert torch.equal(R1[keep], clean[0][keep]) and torch.equal(X[keep], clean[1][keep])
+        assert torch.isnan(R1[2]).all() and torch.isnan(X[2]).all()
+        g = n.join_bwd(cfg, ws, None, S, clean[0], dX, R, gate=G)
+        h = n.join_bwd(cfg, ws, None, B, clean[0], dX, R, gate=G)
+        assert torch.isnan(g["dB"][2]).all() and torch.isnan(g["dgate"][2]).all()
+        assert torch.equal(g["dR"], h["dR"]) and torch.equal(g["dB"][keep], h["dB"][keep])
