@@ -120,8 +120,8 @@ const char *norm_status_string(int status);
 /* Validates a config on the host.  Returns NORM_OK or NORM_ECONFIG. */
 int norm_config_check(const norm_config *cfg);
 
-/* Bytes of workspace that the backward of cfg needs (host output `bytes`):
- * parts of the sums over t, at most 10,300 a column. */
+/* Bytes of workspace that the backward of cfg needs (host output `bytes`), whatever T
+ * is: 10,248 (parts of the sums over t) times D rounded up to 4, rounded up to 256. */
 int norm_workspace_bytes(const norm_config *cfg, uint64_t *bytes);
 
 /* X = norm(R; w, b); the config's gate, scale and options are not looked at.

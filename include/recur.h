@@ -114,7 +114,10 @@ const char *recur_status_string(int status);
 int recur_config_check(const recur_config *cfg);
 
 /* Bytes of workspace that a pass of cfg needs (host output `bytes`); one of the
- * backward's size serves both.  About 2 / 5 D max_tokens bytes (forward: 1 / 7). */
+ * backward's size serves both.  With n pieces of 32 positions in max_tokens (forward:
+ * of 64; a single one up to 128, forward 256) and E = D rounded up to 128:
+ * 256 ceil(D / 64) + 8 E (n + floor(n / 16) + 1), and for the backward 4 D n, rounded
+ * up to 256.  Of wide rows that is 2 / 5 D max_tokens bytes (forward: 1 / 7). */
 int recur_workspace_bytes(const recur_config *cfg, int pass, uint64_t *bytes);
 
 /* Bytes of `saved` for T positions: 4 D ceil(T / RECUR_CHUNK). */
