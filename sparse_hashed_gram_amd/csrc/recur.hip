@@ -813,7 +813,10 @@ __global__ __launch_bounds__(1024) void dlam_kernel(Args a)
 // The rows of one slot: whether `row` is the first of them (it takes them all, in
 // order), and `more`: whether others follow.  Eight loads of 64 slots at a time, the last
 // slot again behind the end: as many for every lane, or the rest would be loaded one by
-// one (500 rows of 2,048 channels: 8.9 us instead of 6.6; without looking 5.5).
+// one (500 rows of 2,048 channels: 8.9 us instead of 6.6; without looking 5.5).  Every
+// wavefront looks at all n slots, so many rows cost n^2: calls of 768 channels take 9.4 us
+// for 1,024 rows, 13.5 for 2,048, 33 for 4,096, 340 for 16,384 and 5,030 for 65,536,
+// without slots 8.6, 8.2, 11, 33 and 149.
 __device__ __forceinline__ bool first_of_slot(const int32_t *slots, int n, int row, int slot, int lane, bool &more)
 {
     bool before = false, behind = false;
@@ -831,6 +834,25 @@ __device__ __forceinline__ bool first_of_slot(const int32_t *slots, int n, int r
     }
     more = __any(behind);
     return !__any(before);
+}
+
+// The next row of the slot behind `row`, n if there is none.  (Slot by slot instead: 44 us
+// instead of 9.3 for 500 rows of which each two share a slot, 600 instead of 44 for 4,096.)
+__device__ __forceinline__ int next_of_slot(const int32_t *slots, int n, int row, int slot, int lane)
+{
+    for (int at = row + 1; at < n; at += 512) {
+        int32_t s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s[i] = slots[min(at + i * 64 + lane, n - 1)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t hit = __ballot(s[i] == slot && at + i * 64 + lane < n);
+            if (hit)
+                return at + i * 64 + __builtin_ctzll(hit);
+        }
+    }
+    return n;
 }
 
 // A wavefront takes a row and V channels a lane; D is a multiple of V: the state is read
@@ -880,9 +902,7 @@ __global__ __launch_bounds__(256) void step_kernel(Args a, float *state, int sta
         store<E, V>(a.y + t * y + off, h);
         if (!more)
             break;
-        do
-            ++t;
-        while (t < n && slots[t] != slot);
+        t = next_of_slot(slots, n, t, slot, lane);
         if (t >= n)
             break;
         x = load<E, V>(a.x + t * a.ldx + off);
