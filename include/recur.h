@@ -44,7 +44,9 @@
  * The workspace holds nothing between calls: calls that share one must be
  * ordered (one stream), and graphs that were captured with the same one must
  * not run at the same time.  Results are the same, bit for bit, in every run of
- * the same call.
+ * the same call.  Blocks of a call wait for states of others that have begun before
+ * them; a wait ends after 2^20 looks, over half a second, which takes a workspace that
+ * something else writes meanwhile, and the values behind it are NaN then.
  */
 #ifndef RECUR_H
 #define RECUR_H
