@@ -1,5 +1,6 @@
 """Loading of the library, shared by the bindings, and the checks of tensors and
-the stream of a call of ``drop``, ``ffn`` and ``ngram.embed_fwd_drop``.
+the stream of a call of ``drop``, ``ffn``, ``norm``, ``recur`` and
+``ngram.embed_fwd_drop``.
 
 A call runs on its tensors' device, on that device's current stream, whatever
 device is current in the calling thread."""
