@@ -942,7 +942,9 @@ int64_t saved_rows(int64_t T) { return (T + RECUR_CHUNK - 1) / RECUR_CHUNK; }
 // Wavefronts of a block: the usual ones, or many where a call that they have not room
 // for is then one chunk, with no words to clear and nobody to wait for (calls back to
 // back, 768 channels: forward of 100 positions 11.6 us instead of 14.6, of 250 11.5 instead
-// of 14.3, forward and backward of 100 26.4 instead of 35.1).
+// of 14.3, forward and backward of 100 26.4 instead of 35.1; without the results' allocation,
+// 64 to 8,192 channels alike: forward of 250 8.5 to 9.2 instead of 11.0 to 11.4, backward of
+// 40 and 120 11.5 to 12.1 instead of 18.1 to 18.4).
 int waves(int pass, int64_t T)
 {
     const int steps = pass == RECUR_PASS_FWD ? kFwdSteps : kBwdSteps;
@@ -956,7 +958,10 @@ uint64_t align_up(uint64_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 // have none, and for as few blocks (or rows of a step) that twice as many still run at once
 // (backward of 2,048 x 768 bf16, 384 blocks: 13.8 us instead of 16.0; of 3,000, 564: 20.2
 // instead of 19.8; forward of 4,096, 384: 12.8 instead of 15.1; of 6,000, 564: 19.6 instead
-// of 18.7; backward of 49,152: 196 instead of 171).
+// of 18.7; backward of 49,152: 196 instead of 171).  At 256, 2,048 and 8,192 channels one is
+// within 2 % of two or faster up to 400 blocks as well (calls of 12,800 x 256 17.9 instead of
+// 23.1, 1,600 x 2,048 12.5 instead of 13.9, 384 x 8,192 11.3 instead of 12.4), and of 256 channels
+// further on (28,800 forward 31.6 instead of 41.3): there the limit gives time away.
 constexpr int64_t kFewBlocks = 400;
 int per_lane(int D, int64_t rows) { return D <= 64 || rows * ((D + 127) / 128) <= kFewBlocks ? 1 : 2; }
 // Of a pass: one too where the call is one chunk, whose 1,024 threads have 128 registers,
