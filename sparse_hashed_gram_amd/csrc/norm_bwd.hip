@@ -6,8 +6,8 @@
 //
 // HBM bounds it at many rows: the norm of 49,152 x 768 takes 102 us of kernel (528 MB,
 // 5.2 TB/s), the join with a gate an element 161 us (830 MB, 5.1 TB/s).  4,099 x 1,001 in
-// fp32 with all gradients: 32 us (3.6 TB/s), 4 rows a block at a time and five turns of which
-// the last has three rows.
+// fp32 with all gradients: 32 to 34 us (3.4 to 3.6 TB/s), 4 rows a block at a time and five
+// turns of which the last has three rows.
 #include <algorithm>
 
 #include "norm_dev.hpp"

@@ -2,7 +2,7 @@
 // R1 = s R + g norm(B), X = norm(R1), in one pass over the rows: a row lives in
 // registers between its loads and its stores, the block's next rows are on their way
 // meanwhile.  HBM bounds it: the join of 49,152 x 768 with a gate an element, bf16
-// beside an fp32 stream, takes 101 us (528 MB, 5.2 TB/s; a copy reaches 5.0 to 5.2).
+// beside an fp32 stream, takes 100 us (528 MB, 5.3 TB/s; a copy reaches 5.0 to 5.2).
 // One row takes 2.1 us of kernel and 7.7 with the call.
 #include <algorithm>
 

@@ -7,8 +7,8 @@
 // input is read once and every output written once; the backward gets its states from
 // one that the forward saved every 32 positions.
 //
-// Measured (bf16, 768 channels): forward of 131,072 positions 225 us (3.6 TB/s), of
-// 49,152 87 us (3.5 TB/s); backward of 49,152 171 us (3.1 TB/s).  What bounds it is the
+// Measured (bf16, 768 channels): forward of 131,072 positions 224 us (3.6 TB/s), of
+// 49,152 86 us (3.5 TB/s); backward of 49,152 168 us (3.1 TB/s).  What bounds it is the
 // time from a chunk's stretch to the state in front of it, two trips through memory
 // that other blocks on the compute unit cover in part: without tickets and words the
 // same kernels take 67 and 127 us, their vector instructions alone 43 and 85.  Hence
