@@ -31,7 +31,8 @@
  * rounded once (bf16: nearest, ties to even).  X is the norm of R1 as it is
  * before it is rounded to r_dtype; the backward takes R1 as it was stored.  A row
  * whose squares pass fp32's range is normalised all the same, with LAYER to 0 where
- * all its values are one.  The norm of a row with a NaN or an infinity is NaN, all of
+ * all its values are equal.  (Otherwise the mean is rounded to fp32: deviations below
+ * some 2^-22 of it are noise.)  The norm of a row with a NaN or an infinity is NaN, all of
  * it, and with it the row's gradient and the sums over t that its xh is in; no other row.
  *
  * Conventions: device pointers unless marked "host"; the caller owns every
